@@ -19,16 +19,18 @@ LIB_PATH = os.path.join(_HERE, "libtq.so")
 (TQ_OK, TQ_ERR_SHAPE, TQ_ERR_ALIGN, TQ_ERR_NULL, TQ_ERR_ARCH, TQ_ERR_WORKSPACE, TQ_ERR_CUDA, TQ_ERR_TIMEOUT,
  TQ_ERR_SCRATCH, TQ_ERR_VALUE) = range(10)
 TQ_ENCODE_MAX_REFITS = 16
-TQ_F32, TQ_F16 = 0, 1
+TQ_F32, TQ_F16, TQ_BF16, TQ_E4M3 = range(4)
 OPS = ("q", "k", "v", "o", "gate", "up", "down")
 
 EXPORTS = ("tq_pack_info", "tq_decode", "tq_rht", "tq_gemv_workspace", "tq_gemv", "tq_gemm_workspace", "tq_gemm",
            "tq_workspace_init", "tq_stack_phase_seed", "tq_layer_phase_workspace", "tq_layer_stack_workspace",
            "tq_layer_phase", "tq_layer_stack", "tq_status_string", "tq_last_cuda_error", "tq_gemv_noalloc",
            "tq_layer_stack_buffers", "tq_layer_stack_outputs", "tq_encode", "tq_ldlq_workspace", "tq_ldlq_encode",
-           "tq_layer_stack_ex", "tq_workspace_status", "tq_gemm_ex")
+           "tq_layer_stack_ex", "tq_workspace_status", "tq_gemm_ex", "tq_kv_append_workspace", "tq_kv_append",
+           "tq_attn_workspace", "tq_attn", "tq_lora_workspace", "tq_lora")
 TQ_STATUS_OFFSET = 65532
 TQ_GEMV_MAX_K = 53760
+TQ_LORA_MAX_RANK = 128
 
 
 class TqError(RuntimeError):
@@ -60,6 +62,20 @@ class tq_stack_options_t(ctypes.Structure):
     _fields_ = [("spin_limit", ctypes.c_uint32), ("test_skip_arrive", ctypes.c_int32)]
 
 
+class tq_kv_cache_t(ctypes.Structure):
+    _fields_ = [("k_d", ctypes.c_void_p), ("v_d", ctypes.c_void_p), ("pages_d", ctypes.c_void_p),
+                ("k_scale_d", ctypes.c_void_p), ("v_scale_d", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class tq_lora_t(ctypes.Structure):
+    _fields_ = [("a_d", ctypes.c_void_p), ("b_d", ctypes.c_void_p), ("scale_d", ctypes.c_void_p),
+                ("dtype", ctypes.c_int32), ("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("n", ctypes.c_int32), ("k", ctypes.c_int32)]
+
+
 _L = None
 
 
@@ -72,6 +88,7 @@ def _lib():
         vp, i32, i64, u64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_size_t
         W = ctypes.POINTER(tq_weight_t)
         LY = ctypes.POINTER(tq_layer_t)
+        KV, LO = ctypes.POINTER(tq_kv_cache_t), ctypes.POINTER(tq_lora_t)
         szp = ctypes.POINTER(ctypes.c_size_t)
         sig = {
             "tq_pack_info": ([i32, i32, ctypes.POINTER(tq_pack_info_t)], ctypes.c_int),
@@ -97,6 +114,12 @@ def _lib():
             "tq_encode": ([vp, i32, i32, vp, ctypes.c_float, i32, vp, vp, vp, vp], ctypes.c_int),
             "tq_ldlq_workspace": ([i32, i32, szp], ctypes.c_int),
             "tq_ldlq_encode": ([vp, i32, i32, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, sz, vp], ctypes.c_int),
+            "tq_kv_append_workspace": ([szp], ctypes.c_int),
+            "tq_kv_append": ([KV, vp, i64, i32, i32, vp, vp, vp, i32, i32, vp, vp, sz, vp], ctypes.c_int),
+            "tq_attn_workspace": ([KV, i32, i32, szp], ctypes.c_int),
+            "tq_attn": ([KV, vp, i32, i32, vp, vp, ctypes.c_float, i32, vp, i32, vp, sz, vp], ctypes.c_int),
+            "tq_lora_workspace": ([LO, i32, szp], ctypes.c_int),
+            "tq_lora": ([LO, vp, i32, vp, vp, i64, vp, i64, vp, sz, vp], ctypes.c_int),
             "tq_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "tq_last_cuda_error": ([], ctypes.c_int),
         }
@@ -104,7 +127,6 @@ def _lib():
             f = getattr(L, name)
             f.argtypes = args
             f.restype = res
-        _ = i64
         _L = L
     return _L
 
@@ -362,3 +384,206 @@ def tq_ldlq_encode(w_rot, u, codebook, gain: float, refits: int = 1, codes=None,
     _ok(_lib().tq_ldlq_encode(_ptr(w_rot), n, k, _ptr(u), _ptr(codebook), float(gain), int(refits), _ptr(codes),
                               _ptr(scales), _ptr(err), _ptr(ws), ws.numel(), _stream(stream)), "tq_ldlq_encode")
     return codes, scales, err
+
+
+# ---- attention between the phases, adapters beside a projection --------------------
+
+def _code(dtype) -> int:
+    """TQ_* code of a torch dtype (None: not a type of these calls)."""
+    import torch
+    return {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16, torch.float8_e4m3fn: TQ_E4M3}.get(dtype)
+
+
+def _need(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type, shape and device (ValueError otherwise)."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (strided)"))
+
+
+def _need_ws(ws, device):
+    import torch
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous uint8 tensor on {device} is needed")
+
+
+class _on:
+    """Make the tensors' device current, and the given stream too (so that what a call allocates belongs to the
+    stream it runs on)."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError(f"a CUDA tensor is needed, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.dev = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.dev.__enter__()
+        self.stream.__enter__()
+
+    def __exit__(self, *a):
+        self.stream.__exit__(*a)
+        self.dev.__exit__(*a)
+
+
+class KvCache:
+    """Caller-owned paged key/value cache.
+
+    k, v: [n_pages][page_size][kv_heads][head_dim] tensors or views (float16,
+    bfloat16 or float8_e4m3fn) with equal strides and a contiguous last
+    dimension; another memory order, such as [page][head][token][d], is given
+    as a permuted view.  pages: int32 [n_seqs][max_pages], contiguous.
+    k_scale, v_scale: float32 [kv_heads], for float8_e4m3fn caches."""
+
+    def __init__(self, k, v, pages, k_scale=None, v_scale=None):
+        import torch
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("k and v: [n_pages][page_size][kv_heads][head_dim] tensors of one type, shape and device")
+        if _code(k.dtype) is None:
+            raise ValueError(f"cache of type {k.dtype}: float16, bfloat16 or float8_e4m3fn is needed")
+        strides = [tuple(0 if n == 1 else st for n, st in zip(t.shape[:3], t.stride()[:3])) for t in (k, v)]
+        if strides[0] != strides[1] or k.stride(3) != 1 or v.stride(3) != 1:
+            raise ValueError("k and v need equal strides and a contiguous last dimension")
+        if pages.dim() != 2:
+            raise ValueError("pages: an int32 [n_seqs][max_pages] tensor is needed")
+        _need(pages, "pages", torch.int32, pages.shape, k.device)
+        _need(k_scale, "k_scale", torch.float32, (k.shape[2],), k.device)
+        _need(v_scale, "v_scale", torch.float32, (k.shape[2],), k.device)
+        self.k, self.v, self.pages, self.k_scale, self.v_scale = k, v, pages, k_scale, v_scale
+        self.device = k.device
+        self.kv_heads, self.head_dim = k.shape[2], k.shape[3]
+        self.q_dtype = torch.bfloat16 if k.dtype == torch.bfloat16 else torch.float16
+        self._struct = tq_kv_cache_t(k.data_ptr(), v.data_ptr(), pages.data_ptr(),
+                                     None if k_scale is None else k_scale.data_ptr(),
+                                     None if v_scale is None else v_scale.data_ptr(), *strides[0], _code(k.dtype),
+                                     k.shape[0], k.shape[1], k.shape[2], k.shape[3], pages.shape[0], pages.shape[1])
+
+    def struct(self) -> tq_kv_cache_t:
+        return self._struct
+
+
+class Lora:
+    """Caller-owned adapters: a [n_adapters][rank][k], b [n_adapters][n][rank]
+    (bfloat16 or float16, contiguous), scale float32 [n_adapters] or None."""
+
+    def __init__(self, a, b, scale=None):
+        import torch
+        if a.dim() != 3 or b.dim() != 3 or a.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("a [n_adapters][rank][k] and b [n_adapters][n][rank] of float16 or bfloat16 are needed")
+        _need(a, "a", a.dtype, a.shape, a.device)
+        _need(b, "b", a.dtype, (a.shape[0], b.shape[1], a.shape[1]), a.device)
+        _need(scale, "scale", torch.float32, (a.shape[0],), a.device)
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self.n_adapters, self.rank, self.k = a.shape
+        self.n = b.shape[1]
+        self._struct = tq_lora_t(a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(),
+                                 _code(a.dtype), self.n_adapters, self.rank, self.n, self.k)
+
+    def struct(self) -> tq_lora_t:
+        return self._struct
+
+
+def tq_kv_append_workspace() -> int:
+    b = ctypes.c_size_t()
+    _ok(_lib().tq_kv_append_workspace(ctypes.byref(b)), "tq_kv_append_workspace")
+    return b.value
+
+
+def tq_kv_append(cache: KvCache, qkv, q_heads: int, pos, freq=None, interleaved: bool = False, seq=None, q_out=None,
+                 ws=None, stream=None):
+    """Rotate and append new tokens.  qkv: float32 [m][(q_heads + 2 kv_heads) head_dim] (rows may be strided), pos:
+    int32 [m] (-1 = a padded row), freq: float64 [rot/2] radians per position (None: no rotation), seq: int32 [m]
+    rows of the block table (None: token t is sequence t).  Returns the rotated queries [m][q_heads][head_dim]
+    (bfloat16 for a bfloat16 cache, else float16)."""
+    import torch
+    dev, m = cache.device, qkv.shape[0]
+    if (qkv.dim() != 2 or qkv.dtype != torch.float32 or qkv.device != dev or qkv.stride(1) != 1
+            or qkv.shape[1] != (q_heads + 2 * cache.kv_heads) * cache.head_dim):
+        raise ValueError(f"qkv: float32 rows of {q_heads} + 2 x {cache.kv_heads} heads of {cache.head_dim} on {dev} are "
+                         "needed")
+    _need(pos, "pos", torch.int32, (m,), dev)
+    _need(seq, "seq", torch.int32, (m,), dev)
+    half = 0 if freq is None else freq.numel()
+    _need(freq, "freq", torch.float64, (half,), dev)
+    _need(q_out, "q_out", cache.q_dtype, (m, q_heads, cache.head_dim), dev)
+    if seq is None and m > cache.pages.shape[0]:
+        raise ValueError(f"{m} tokens without seq, but the block table has {cache.pages.shape[0]} rows")
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((m, q_heads, cache.head_dim), dtype=cache.q_dtype, device=dev)
+        if ws is None:
+            ws = workspace(tq_kv_append_workspace(), dev)
+        _need_ws(ws, dev)
+        row = qkv.shape[1] if m == 1 else qkv.stride(0)
+        _ok(_lib().tq_kv_append(ctypes.byref(cache.struct()), _ptr(qkv), row, m, q_heads, _ptr(seq), _ptr(pos),
+                                _ptr(freq), 2 * half, int(bool(interleaved)), _ptr(q_out), _ptr(ws), ws.numel(),
+                                _stream()), "tq_kv_append")
+    return q_out
+
+
+def tq_attn_workspace(cache: KvCache, m: int, q_heads: int) -> int:
+    b = ctypes.c_size_t()
+    _ok(_lib().tq_attn_workspace(ctypes.byref(cache.struct()), m, q_heads, ctypes.byref(b)), "tq_attn_workspace")
+    return b.value
+
+
+def tq_attn(cache: KvCache, q, pos, scale: float, seq=None, window: int = 0, out=None, out_dtype: int = TQ_BF16, ws=None,
+            stream=None):
+    """Attention of new tokens over the cache.  q: [m][q_heads][head_dim] (tq_kv_append's output), pos: int32 [m], the
+    last visible position of each row (-1 = none), window: only the last `window` positions (0 = all).  Returns
+    [m][q_heads][head_dim], bfloat16 (the input of the o projection) or float16."""
+    import torch
+    dev = cache.device
+    if q.dim() != 3:
+        raise ValueError("q: [m][q_heads][head_dim] is needed")
+    m, q_heads = q.shape[:2]
+    _need(q, "q", cache.q_dtype, (m, q_heads, cache.head_dim), dev)
+    _need(pos, "pos", torch.int32, (m,), dev)
+    _need(seq, "seq", torch.int32, (m,), dev)
+    if seq is None and m > cache.pages.shape[0]:
+        raise ValueError(f"{m} rows without seq, but the block table has {cache.pages.shape[0]} rows")
+    if out is not None:
+        _need(out, "out", torch.float16 if out.dtype == torch.float16 else torch.bfloat16, q.shape, dev)
+        out_dtype = _code(out.dtype)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, device=dev)
+        if ws is None:
+            ws = workspace(tq_attn_workspace(cache, m, q_heads), dev)
+        _need_ws(ws, dev)
+        _ok(_lib().tq_attn(ctypes.byref(cache.struct()), _ptr(q), m, q_heads, _ptr(seq), _ptr(pos), float(scale),
+                           int(window), _ptr(out), out_dtype, _ptr(ws), ws.numel(), _stream()), "tq_attn")
+    return out
+
+
+def tq_lora_workspace(lora: Lora, m: int) -> int:
+    b = ctypes.c_size_t()
+    _ok(_lib().tq_lora_workspace(ctypes.byref(lora.struct()), m, ctypes.byref(b)), "tq_lora_workspace")
+    return b.value
+
+
+def tq_lora(lora: Lora, x, adapter, y, out=None, ws=None, stream=None):
+    """out = y + scale[a] B[a] A[a] x per token.  x: [m][k] of the adapters' type, adapter: int32 [m] (-1 = none), y:
+    float32 [m][n] (rows may be strided: columns of a wider output).  out: where to write (None: y itself)."""
+    import torch
+    dev, m = lora.device, x.shape[0]
+    _need(x, "x", lora.a.dtype, (m, lora.k), dev)
+    _need(adapter, "adapter", torch.int32, (m,), dev)
+    out = y if out is None else out
+    for name, t in (("y", y), ("out", out)):
+        if t.dtype != torch.float32 or tuple(t.shape) != (m, lora.n) or t.device != dev or (
+                t.numel() and lora.n > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: float32 [{m}][{lora.n}] with contiguous rows on {dev} is needed")
+    with _on(dev, stream):
+        if ws is None:
+            ws = workspace(tq_lora_workspace(lora, m), dev)
+        _need_ws(ws, dev)
+        ys, os_ = (lora.n if m <= 1 else t.stride(0) for t in (y, out))
+        _ok(_lib().tq_lora(ctypes.byref(lora.struct()), _ptr(x), m, _ptr(adapter), _ptr(y), ys, _ptr(out), os_, _ptr(ws),
+                           ws.numel(), _stream()), "tq_lora")
+    return out

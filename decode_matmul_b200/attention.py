@@ -1,0 +1,118 @@
+"""Layer stack with its attention: the four phases of every layer, with the
+rotated keys and values appended to a paged cache after phase 0 and the
+attention of the new tokens over that cache as phase 1's input.
+
+Where `tq_layer_stack` hands alpha * q straight to phase 1 (its k and v
+outputs only stand in for attention), one layer here is
+
+    y   = q|k|v of RHT(h)                          tq_layer_phase, phase 0
+    y  += adapters of each token on q, k, v        tq_lora (optional)
+    q'  = rotated q; cache <- rotated k, v         tq_kv_append
+    a   = attention of q' over the cache           tq_attn (bf16)
+    h   = phases 1, 2, 3 of a                      tq_layer_phase
+
+Every call is enqueued on the current stream and none synchronises, so a
+decode step can be captured in a CUDA graph: positions, sequences and adapters
+are read on the device, and a replay with new values in the same tensors is
+the next step.
+"""
+from __future__ import annotations
+
+PHASE_OPS = (("q", "k", "v"), ("o",), ("gate", "up"), ("down",))
+
+
+class AttentionStack:
+    """layers: one dict per layer of DeviceWeights (q, k, v, o, gate, up,
+    down).  caches: one KvCache per layer (all with the same heads).  freq:
+    float64 [rot/2] rotation frequencies (None: no rotation).  scale: of the
+    scores (None: head_dim ** -0.5).  window: of the attention (0: all keys).
+    adapters: None, or one dict per layer of Lora by op name ("q", "k", "v"),
+    bfloat16, over the phase's unrotated input."""
+
+    def __init__(self, layers, caches, freq=None, interleaved: bool = False, scale=None, window: int = 0,
+                 adapters=None):
+        from . import layer_struct
+        if len(caches) != len(layers) or (adapters is not None and len(adapters) != len(layers)):
+            raise ValueError("one cache (and one dict of adapters) per layer is needed")
+        c, w = caches[0], layers[0]
+        self.q_heads, rest = divmod(w["q"].n, c.head_dim)
+        if rest or self.q_heads % c.kv_heads:
+            raise ValueError(f"{w['q'].n} query features do not make groups of heads of {c.head_dim}")
+        for L, cache in zip(layers, caches):
+            kv = cache.kv_heads * cache.head_dim
+            if (L["q"].n, L["k"].n, L["v"].n) != (w["q"].n, kv, kv) or cache.head_dim != c.head_dim:
+                raise ValueError("the q, k and v outputs of a layer do not match its cache's heads")
+            if L["o"].k != L["q"].n:
+                raise ValueError("the o projection's input is the q projection's width")
+        for A, L in zip(adapters or (), layers):
+            for op, lora in A.items():
+                if op not in PHASE_OPS[0] or (lora.n, lora.k) != (L[op].n, L[op].k):
+                    raise ValueError(f"adapter on {op!r}: only q, k and v, of their projection's size")
+        self.layers, self.caches, self.freq, self.interleaved, self.window = layers, caches, freq, interleaved, window
+        self.scale = c.head_dim ** -0.5 if scale is None else scale
+        self.adapters = adapters
+        self.device = c.device
+        self.structs = [layer_struct(L) for L in layers]
+        self._buf = {}
+
+    def buffers(self, m: int) -> dict:
+        """The workspace and activation buffers of steps of m tokens (kept; the last layer's values stay in them
+        after a step: y, q, attn and the phases' handoffs)."""
+        if m not in self._buf:
+            import torch
+
+            from . import tq_attn_workspace, tq_layer_phase_workspace, tq_lora_workspace, workspace
+            n = max(tq_layer_phase_workspace(s, p, m) for s in self.structs for p in range(4))
+            n = max([n] + [tq_attn_workspace(c, m, self.q_heads) for c in self.caches]
+                    + [tq_lora_workspace(a, m) for A in self.adapters or () for a in A.values()])
+            w, c, dev = self.layers[0], self.caches[0], self.device
+
+            def bits(width):
+                return torch.empty((m, width), dtype=torch.int16, device=dev)
+
+            heads = (m, self.q_heads, c.head_dim)
+            self._buf[m] = dict(
+                ws=workspace(n, dev), y=torch.empty((m, sum(w[o].n for o in PHASE_OPS[0])), device=dev),
+                q=torch.empty(heads, dtype=c.q_dtype, device=dev),
+                attn=torch.empty(heads, dtype=torch.bfloat16, device=dev),
+                hand=[bits(w["q"].n), bits(w["o"].n), bits(w["gate"].n), bits(w["down"].n)])
+        return self._buf[m]
+
+    def forward(self, h, pos, seed: int, seq=None, adapter=None, out=None):
+        """One step of m new tokens.  h: int16 (bf16 bits) [m][hidden]; pos: int32 [m], the tokens' positions (-1 = a
+        padded row); seq: int32 [m], their rows of the block tables (None: token t is sequence t); adapter: int32 [m]
+        (-1 = none), needed with adapters.  Writes the caches and returns the last hidden state, int16 [m][hidden]
+        (`out` if given, which may be h; else a new tensor).  An index out of range shows in
+        tq_workspace_status(buffers(m)["ws"])."""
+        import torch
+
+        from . import tq_attn, tq_kv_append, tq_layer_phase, tq_lora, tq_stack_phase_seed
+        if self.adapters is not None and adapter is None:
+            raise ValueError("adapter: int32 [m] is needed, since the stack has adapters")
+        m = h.shape[0]
+        if h.dtype != torch.int16 or h.shape[1] != self.layers[0]["q"].k or not h.is_contiguous() or h.device != self.device:
+            raise ValueError(f"h: contiguous int16 [m][{self.layers[0]['q'].k}] on {self.device} is needed")
+        if out is None:
+            out = torch.empty_like(h)
+        if m == 0:
+            return out
+        b = self.buffers(m)
+        ws, y, hand = b["ws"], b["y"], b["hand"]
+        with torch.cuda.device(self.device):
+            x = h
+            for l, (s, w, cache) in enumerate(zip(self.structs, self.layers, self.caches)):
+                tq_layer_phase(s, 0, x, tq_stack_phase_seed(seed, l, 0), y, hand[0], ws)
+                col = 0
+                for op in PHASE_OPS[0]:
+                    lora = self.adapters[l].get(op) if self.adapters is not None else None
+                    if lora is not None:
+                        tq_lora(lora, x.view(torch.bfloat16), adapter, y[:, col:col + w[op].n], ws=ws)
+                    col += w[op].n
+                tq_kv_append(cache, y, self.q_heads, pos, self.freq, self.interleaved, seq, b["q"], ws)
+                tq_attn(cache, b["q"], pos, self.scale, seq, self.window, b["attn"], ws=ws)
+                x = b["attn"].view(torch.int16).view(m, -1)
+                for p in (1, 2, 3):
+                    to = out if p == 3 and l + 1 == len(self.layers) else hand[p]
+                    tq_layer_phase(s, p, x, tq_stack_phase_seed(seed, l, p), None, to, ws)
+                    x = to
+        return out

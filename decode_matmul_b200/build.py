@@ -12,7 +12,7 @@ LIB = os.path.join(HERE, "libtq.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
          "-shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-         "--expt-relaxed-constexpr"]
+         "--expt-relaxed-constexpr", "-t", "0"]
 
 
 def sources():

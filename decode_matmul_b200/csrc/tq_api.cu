@@ -9,6 +9,7 @@
 #include "tq_decode.cuh"
 #include "tq_dmma.cuh"
 #include "tq_encode.cuh"
+#include "tq_host.cuh"
 #include "tq_rht.cuh"
 #include "tq_stack1.cuh"
 #include "tq_stackn.cuh"
@@ -16,44 +17,9 @@
 
 #include <cudaTypedefs.h>
 
+using namespace tq_host;
+
 namespace {
-
-thread_local int g_last_cuda_error = 0;
-
-int cuda_fail(cudaError_t e) {
-  g_last_cuda_error = (int)e;
-  return TQ_ERR_CUDA;
-}
-
-#define TQ_CUDA(call)                           \
-  do {                                          \
-    cudaError_t e_ = (call);                    \
-    if (e_ != cudaSuccess) return cuda_fail(e_); \
-  } while (0)
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr int kMaxDevices = 64;
-int g_arch_ok[kMaxDevices];  // 0 unknown, 1 ok, 2 bad
-int g_num_sms[kMaxDevices];
-
-// Current device must be compute capability 10.0 (B200, sm_100a).
-int check_arch(int* num_sms) {
-  int dev = 0;
-  TQ_CUDA(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= kMaxDevices) return TQ_ERR_ARCH;
-  if (g_arch_ok[dev] == 0) {
-    int major = 0, minor = 0, sms = 0;
-    TQ_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev));
-    TQ_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev));
-    TQ_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    g_num_sms[dev] = sms;
-    g_arch_ok[dev] = (major == 10 && minor == 0) ? 1 : 2;
-  }
-  if (g_arch_ok[dev] != 1) return TQ_ERR_ARCH;
-  if (num_sms) *num_sms = g_num_sms[dev];
-  return TQ_OK;
-}
 
 bool k_ok(int32_t k) { return k > 0 && k % 512 == 0; }
 
@@ -63,28 +29,6 @@ int check_weight(const tq_weight_t* w) {
   if (!w->codes_d || !w->scales_d || !w->codebook_d) return TQ_ERR_NULL;
   if (!aligned16(w->codes_d) || !aligned16(w->codebook_d)) return TQ_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(w->scales_d) & 3) return TQ_ERR_ALIGN;  // read two blocks' scales at a time
-  return TQ_OK;
-}
-
-// Launch with the programmatic-stream-serialization attribute so that a
-// kernel may start its weight prefetch while the previous one finishes.
-template <typename... KArgs, typename... Args>
-int launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-#ifdef TQ_NO_PDL
-  cfg.numAttrs = 0;  // build option: plain stream ordering
-#else
-  cfg.numAttrs = 1;
-#endif
-  TQ_CUDA(cudaLaunchKernelEx(&cfg, kernel, args...));
   return TQ_OK;
 }
 
@@ -106,11 +50,6 @@ struct DmmaWs {
   size_t counters_off, partials_off, bytes;
 };
 
-// Every workspace starts with a fixed region of per-tile arrival counters
-// (kCounterBytes, so every call, whatever its shape, finds its counters in
-// the same zeroed bytes; each call leaves them zero).  Everything after it
-// (partial sums, activation scratch) is written before it is read.
-constexpr size_t kCounterBytes = 64 * 1024;
 constexpr int64_t kMaxTiles = kCounterBytes / 4 - 1;  // the last slot holds the status word
 
 DmmaWs dmma_ws_layout(int64_t n_total, int32_t k, int mc) {

@@ -1,0 +1,247 @@
+// tq_serve.cu -- the C ABI's paged cache, attention and adapter entry points
+// (see include/tq.h): argument checks and launches.  No allocation, no
+// synchronisation.
+#include <math.h>
+#include <string.h>
+
+#include "../../include/tq.h"
+#include "tq_attn.cuh"
+#include "tq_host.cuh"
+#include "tq_kv.cuh"
+#include "tq_lora.cuh"
+
+using namespace tq_host;
+
+namespace {
+
+constexpr int32_t kMaxM = 4096;  // tokens per call, as in tq_gemm
+
+int32_t* status_word(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + TQ_STATUS_OFFSET); }
+
+bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int check_cache(const tq_kv_cache_t* c) {
+  if (!c) return TQ_ERR_NULL;
+  if (c->dtype != TQ_F16 && c->dtype != TQ_BF16 && c->dtype != TQ_E4M3) return TQ_ERR_VALUE;
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128 && c->head_dim != 256) return TQ_ERR_SHAPE;
+  if (c->n_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->n_seqs < 1 || c->max_pages < 1) return TQ_ERR_SHAPE;
+  if ((int64_t)c->page_size * c->max_pages > 0x7fffffff) return TQ_ERR_SHAPE;
+  if (!c->k_d || !c->v_d || !c->pages_d) return TQ_ERR_NULL;
+  const int64_t eb = c->dtype == TQ_E4M3 ? 1 : 2;
+  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0) return TQ_ERR_VALUE;
+  if ((c->page_stride * eb) % 16 || (c->token_stride * eb) % 16 || (c->head_stride * eb) % 16) return TQ_ERR_ALIGN;
+  if (!aligned16(c->k_d) || !aligned16(c->v_d) || !aligned_to(c->pages_d, 4) || !aligned_to(c->k_scale_d, 4) ||
+      !aligned_to(c->v_scale_d, 4))
+    return TQ_ERR_ALIGN;
+  if (c->dtype != TQ_E4M3 && (c->k_scale_d || c->v_scale_d)) return TQ_ERR_VALUE;
+  return TQ_OK;
+}
+
+tq::KvView cache_view(const tq_kv_cache_t* c) {
+  tq::KvView v;
+  v.k = c->k_d;
+  v.v = c->v_d;
+  v.pages = c->pages_d;
+  v.ks = c->k_scale_d;
+  v.vs = c->v_scale_d;
+  v.page_stride = c->page_stride;
+  v.token_stride = c->token_stride;
+  v.head_stride = c->head_stride;
+  v.n_pages = c->n_pages;
+  v.page_size = c->page_size;
+  v.kv_heads = c->kv_heads;
+  v.head_dim = c->head_dim;
+  v.n_seqs = c->n_seqs;
+  v.max_pages = c->max_pages;
+  return v;
+}
+
+int check_heads(const tq_kv_cache_t* c, int32_t m, int32_t q_heads) {
+  if (m < 0 || m > kMaxM) return TQ_ERR_SHAPE;
+  if (q_heads < 1 || q_heads % c->kv_heads != 0) return TQ_ERR_SHAPE;
+  if ((int64_t)(q_heads + 2 * (int64_t)c->kv_heads) * c->head_dim > 1 << 24) return TQ_ERR_SHAPE;
+  return TQ_OK;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return TQ_ERR_WORKSPACE;
+  if (!aligned16(ws)) return TQ_ERR_ALIGN;
+  return TQ_OK;
+}
+
+size_t attn_ws_bytes(const tq_kv_cache_t* c, int32_t m, int32_t q_heads) {
+  (void)c, (void)m, (void)q_heads;
+  return kCounterBytes;
+}
+
+int check_lora(const tq_lora_t* l) {
+  if (!l) return TQ_ERR_NULL;
+  if (l->dtype != TQ_F16 && l->dtype != TQ_BF16) return TQ_ERR_VALUE;
+  if (l->n_adapters < 1 || l->n < 1 || l->k < 512 || l->k % 512 != 0) return TQ_ERR_SHAPE;
+  if (l->rank < 8 || l->rank > TQ_LORA_MAX_RANK || l->rank % 8 != 0) return TQ_ERR_SHAPE;
+  if (!l->a_d || !l->b_d) return TQ_ERR_NULL;
+  if (!aligned16(l->a_d) || !aligned16(l->b_d) || !aligned_to(l->scale_d, 4)) return TQ_ERR_ALIGN;
+  return TQ_OK;
+}
+
+size_t lora_ws_bytes(const tq_lora_t* l, int32_t m) { return kCounterBytes + (size_t)m * l->rank * sizeof(float); }
+
+}  // namespace
+
+extern "C" {
+
+int tq_kv_append_workspace(size_t* bytes) {
+  if (!bytes) return TQ_ERR_NULL;
+  *bytes = kCounterBytes;
+  return TQ_OK;
+}
+
+int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t qkv_stride, int32_t m, int32_t q_heads,
+                 const int32_t* seq_d, const int32_t* pos_d, const double* freq_d, int32_t rot_dim,
+                 int32_t interleaved, void* q_out_d, void* workspace_d, size_t ws_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st != TQ_OK) return st;
+  st = check_heads(cache, m, q_heads);
+  if (st != TQ_OK) return st;
+  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 16 != 0) return TQ_ERR_SHAPE;
+  if (interleaved != 0 && interleaved != 1) return TQ_ERR_VALUE;
+  if (qkv_stride < (int64_t)(q_heads + 2 * cache->kv_heads) * cache->head_dim) return TQ_ERR_SHAPE;
+  if (m == 0) return TQ_OK;
+  if (!qkv_d || !pos_d || !q_out_d || (rot_dim > 0 && !freq_d)) return TQ_ERR_NULL;
+  if (!aligned16(qkv_d) || qkv_stride % 4 != 0 || !aligned16(q_out_d) || !aligned_to(pos_d, 4) ||
+      !aligned_to(seq_d, 4) || !aligned_to(freq_d, 8))
+    return TQ_ERR_ALIGN;
+  st = check_ws(workspace_d, ws_bytes, kCounterBytes);
+  if (st != TQ_OK) return st;
+  int sms = 0;
+  st = check_arch(&sms);
+  if (st != TQ_OK) return st;
+  tq::AppendParams p;
+  p.c = cache_view(cache);
+  p.qkv = qkv_d;
+  p.qkv_stride = qkv_stride;
+  p.q_out = q_out_d;
+  p.seq = seq_d;
+  p.pos = pos_d;
+  p.freq = freq_d;
+  p.m = m;
+  p.q_heads = q_heads;
+  p.rot = rot_dim;
+  p.interleaved = interleaved;
+  p.status = status_word(workspace_d);
+  const int units = (q_heads + 2 * cache->kv_heads) * (cache->head_dim / 16);
+  const int parts = (units + tq::AP_THREADS - 1) / tq::AP_THREADS;
+  const dim3 grid((unsigned)m, (unsigned)parts), block(tq::AP_THREADS);
+  cudaStream_t s = (cudaStream_t)stream;
+  switch (cache->dtype) {
+    case TQ_F16: return launch(tq::append_kernel<tq::KV_F16>, grid, block, 0, s, p);
+    case TQ_BF16: return launch(tq::append_kernel<tq::KV_BF16>, grid, block, 0, s, p);
+    default: return launch(tq::append_kernel<tq::KV_E4M3>, grid, block, 0, s, p);
+  }
+}
+
+int tq_attn_workspace(const tq_kv_cache_t* cache, int32_t m, int32_t q_heads, size_t* bytes) {
+  if (!bytes) return TQ_ERR_NULL;
+  int st = check_cache(cache);
+  if (st != TQ_OK) return st;
+  st = check_heads(cache, m, q_heads);
+  if (st != TQ_OK) return st;
+  *bytes = attn_ws_bytes(cache, m, q_heads);
+  return TQ_OK;
+}
+
+int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_heads, const int32_t* seq_d,
+            const int32_t* pos_d, float scale, int32_t window, void* out_d, int32_t out_dtype, void* workspace_d,
+            size_t ws_bytes, void* stream) {
+  int st = check_cache(cache);
+  if (st != TQ_OK) return st;
+  st = check_heads(cache, m, q_heads);
+  if (st != TQ_OK) return st;
+  if (out_dtype != TQ_F16 && out_dtype != TQ_BF16) return TQ_ERR_VALUE;
+  if (!isfinite(scale) || window < 0) return TQ_ERR_VALUE;
+  if (m == 0) return TQ_OK;
+  if (!q_d || !pos_d || !out_d) return TQ_ERR_NULL;
+  if (!aligned16(q_d) || !aligned16(out_d) || !aligned_to(pos_d, 4) || !aligned_to(seq_d, 4)) return TQ_ERR_ALIGN;
+  st = check_ws(workspace_d, ws_bytes, attn_ws_bytes(cache, m, q_heads));
+  if (st != TQ_OK) return st;
+  int sms = 0;
+  st = check_arch(&sms);
+  if (st != TQ_OK) return st;
+  tq::AttnParams p;
+  p.c = cache_view(cache);
+  p.q = q_d;
+  p.seq = seq_d;
+  p.pos = pos_d;
+  p.out = out_d;
+  p.m = m;
+  p.q_heads = q_heads;
+  p.window = window;
+  p.scale = scale;
+  p.status = status_word(workspace_d);
+  const int64_t items = (int64_t)m * q_heads;
+  const dim3 grid((unsigned)((items + 3) / 4)), block(128);
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool bf = out_dtype == TQ_BF16;
+  switch (cache->dtype) {
+    case TQ_F16:
+      return bf ? launch(tq::attn_kernel<tq::KV_F16, true>, grid, block, 0, s, p)
+                : launch(tq::attn_kernel<tq::KV_F16, false>, grid, block, 0, s, p);
+    case TQ_BF16:
+      return bf ? launch(tq::attn_kernel<tq::KV_BF16, true>, grid, block, 0, s, p)
+                : launch(tq::attn_kernel<tq::KV_BF16, false>, grid, block, 0, s, p);
+    default:
+      return bf ? launch(tq::attn_kernel<tq::KV_E4M3, true>, grid, block, 0, s, p)
+                : launch(tq::attn_kernel<tq::KV_E4M3, false>, grid, block, 0, s, p);
+  }
+}
+
+int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes) {
+  if (!bytes) return TQ_ERR_NULL;
+  int st = check_lora(lora);
+  if (st != TQ_OK) return st;
+  if (m < 0 || m > kMaxM) return TQ_ERR_SHAPE;
+  *bytes = lora_ws_bytes(lora, m);
+  return TQ_OK;
+}
+
+int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* adapter_d, const float* y_d,
+            int64_t y_stride, float* out_d, int64_t out_stride, void* workspace_d, size_t ws_bytes, void* stream) {
+  int st = check_lora(lora);
+  if (st != TQ_OK) return st;
+  if (m < 0 || m > kMaxM || y_stride < lora->n || out_stride < lora->n) return TQ_ERR_SHAPE;
+  if (m == 0) return TQ_OK;
+  if (!x_d || !adapter_d || !y_d || !out_d) return TQ_ERR_NULL;
+  if (!aligned16(x_d) || !aligned_to(adapter_d, 4) || !aligned_to(y_d, 4) || !aligned_to(out_d, 4)) return TQ_ERR_ALIGN;
+  st = check_ws(workspace_d, ws_bytes, lora_ws_bytes(lora, m));
+  if (st != TQ_OK) return st;
+  int sms = 0;
+  st = check_arch(&sms);
+  if (st != TQ_OK) return st;
+  tq::LoraParams p;
+  p.a = lora->a_d;
+  p.b = lora->b_d;
+  p.scale = lora->scale_d;
+  p.x = x_d;
+  p.adapter = adapter_d;
+  p.y = y_d;
+  p.out = out_d;
+  p.y_stride = y_stride;
+  p.out_stride = out_stride;
+  p.n_adapters = lora->n_adapters;
+  p.rank = lora->rank;
+  p.n = lora->n;
+  p.k = lora->k;
+  p.m = m;
+  p.h = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + kCounterBytes);
+  p.status = status_word(workspace_d);
+  cudaStream_t s = (cudaStream_t)stream;
+  const bool bf = lora->dtype == TQ_BF16;
+  st = bf ? launch(tq::lora_shrink_kernel<true>, dim3((unsigned)m), dim3(256), 0, s, p)
+          : launch(tq::lora_shrink_kernel<false>, dim3((unsigned)m), dim3(256), 0, s, p);
+  if (st != TQ_OK) return st;
+  const dim3 grid((unsigned)m, (unsigned)((lora->n + 255) / 256));
+  return bf ? launch(tq::lora_expand_kernel<true>, grid, dim3(256), 0, s, p)
+            : launch(tq::lora_expand_kernel<false>, grid, dim3(256), 0, s, p);
+}
+
+}  // extern "C"

@@ -69,11 +69,15 @@ extern "C" {
 #define TQ_ERR_CUDA 6      /* a CUDA runtime call failed; tq_last_cuda_error() has its code */
 #define TQ_ERR_TIMEOUT 7   /* a bounded device-side wait expired (reported by the status word) */
 #define TQ_ERR_SCRATCH 8   /* the problem does not fit the built-in scratch of tq_gemv_noalloc */
-#define TQ_ERR_VALUE 9     /* a scalar argument (not a size) is out of range */
+#define TQ_ERR_VALUE 9     /* a scalar argument (not a size) is out of range; in the status word: an index in
+                            * device memory (page, sequence, adapter) was out of range */
 
-/* output element types */
+/* element types (outputs of tq_rht: TQ_F32, TQ_F16; caches, attention and
+ * adapters: as each declaration says) */
 #define TQ_F32 0
 #define TQ_F16 1
+#define TQ_BF16 2
+#define TQ_E4M3 3
 
 /* One trellis-coded weight.  All pointers are device pointers (caller-owned).
  * codes_d: uint8 [n][k/4], 16-byte aligned.  scales_d: fp16 bits [n][k/256],
@@ -369,6 +373,127 @@ TQ_API int tq_ldlq_workspace(int32_t n, int32_t k, size_t* bytes);
 TQ_API int tq_ldlq_encode(const float* w_rot_d, int32_t n, int32_t k, const float* u_d, const uint16_t* codebook_d,
                           float gain, int32_t refits, uint8_t* codes_d, uint16_t* scales_d, float* err_d,
                           void* workspace_d, size_t ws_bytes, void* stream);
+
+/* ---- attention between the phases ---------------------------------------------
+ * What stands between phase 0 (q|k|v) and phase 1 (o) of a layer when the
+ * keys and values are kept: the rotation of queries and keys by position and
+ * the append to a paged cache (tq_kv_append), and the attention of new tokens
+ * over it (tq_attn), whose bf16 output is phase 1's input.  The pages stop at
+ * the linear layers; the formulas are stated here.
+ *
+ * Paged cache, all of it caller-owned.  Keys and values lie in pages of
+ * page_size tokens; element (page, i, head, d) of k and of v is at
+ *   page * page_stride + i * token_stride + head * head_stride + d
+ * elements from k_d / v_d, so both [page][token][head][d] and
+ * [page][head][token][d] orders (and caches that interleave k and v) can be
+ * described.  Position j of sequence s is token j % page_size of page
+ * pages_d[s * max_pages + j / page_size].
+ * dtype: TQ_F16, TQ_BF16 or TQ_E4M3.  An e4m3 element stands for its value
+ *   times k_scale_d[head] / v_scale_d[head] (device fp32 [kv_heads], or NULL
+ *   = 1; NULL for the 16-bit types, TQ_ERR_VALUE otherwise).
+ * head_dim: 64, 96, 128 or 256 (TQ_ERR_SHAPE).  page_size, n_pages, n_seqs,
+ *   max_pages, kv_heads >= 1; page_size * max_pages < 2^31.
+ * Strides: >= 0 (TQ_ERR_VALUE) and multiples of 16 bytes; k_d and v_d 16-byte
+ *   aligned (TQ_ERR_ALIGN). */
+typedef struct tq_kv_cache {
+  void* k_d;
+  void* v_d;
+  const int32_t* pages_d;
+  const float* k_scale_d;
+  const float* v_scale_d;
+  int64_t page_stride, token_stride, head_stride;
+  int32_t dtype;
+  int32_t n_pages, page_size, kv_heads, head_dim, n_seqs, max_pages;
+} tq_kv_cache_t;
+
+/* Rotate and append m new tokens.  Token t has the fp32 row
+ * qkv_d[t * qkv_stride ...] of q_heads query, kv_heads key and kv_heads value
+ * heads (phase 0's y), the position pos_d[t] and the sequence seq_d[t]
+ * (seq_d NULL: sequence t).
+ *   query and key heads: pair i of the first rot_dim features (features i and
+ *   i + rot_dim/2, or 2i and 2i+1 with interleaved = 1) becomes
+ *     (a cos u - b sin u, a sin u + b cos u),  u = pos * freq_d[i];
+ *   the features from rot_dim on, and the values, stay as they are.
+ * q_out_d [m][q_heads][head_dim]: bf16 for a bf16 cache, else fp16 (rounded
+ *   to nearest even).  Keys and values go to the cache slot of their position:
+ *   16-bit types rounded to nearest even, e4m3 the nearest value to x / scale
+ *   (ties to even, saturating at +-448; NaN stays NaN).
+ * pos_d[t] < 0 marks a padded row: nothing is stored and its q_out row is 0.
+ * A sequence, position or page outside the table or the cache stores nothing
+ *   and leaves TQ_ERR_VALUE in the workspace's status word (q_out is written).
+ *   Two tokens of a call with the same slot: one of them is kept, which one is
+ *   not specified.  Every other byte of the cache is left as it was.
+ * freq_d: device fp64 [rot_dim/2], radians per position (fp64 so that far
+ *   positions keep their angle); unused when rot_dim is 0.
+ * rot_dim: a multiple of 16, 0 .. head_dim.  qkv_stride: elements, a multiple
+ *   of 4, at least the row's length.  q_heads: a multiple of kv_heads.
+ * qkv_d and q_out_d 16-byte aligned.  0 <= m <= 4096.
+ * workspace_d: at least tq_kv_append_workspace bytes; only the status word is
+ *   used, so it can be the workspace of any other call of the step. */
+TQ_API int tq_kv_append_workspace(size_t* bytes);
+TQ_API int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t qkv_stride, int32_t m, int32_t q_heads,
+                        const int32_t* seq_d, const int32_t* pos_d, const double* freq_d, int32_t rot_dim,
+                        int32_t interleaved, void* q_out_d, void* workspace_d, size_t ws_bytes, void* stream);
+
+/* Attention of m new tokens over the cache.  Row t (query heads q_d[t]) sees
+ * the keys j of sequence seq_d[t] (NULL: t) with j <= pos_d[t], and
+ * j > pos_d[t] - window when window > 0.  Query head h reads key head
+ * h / (q_heads / kv_heads):
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) V_j
+ * q_d: [m][q_heads][head_dim], bf16 for a bf16 cache, else fp16.  out_d: the
+ *   same layout, out_dtype TQ_BF16 (phase 1's input) or TQ_F16.  Scores,
+ *   maxima, sums and outputs are fp32 until the last rounding.
+ * A row that sees no key (pos_d[t] < 0: a padded row) gives zeros.  Cache
+ *   bytes of positions that no row sees are not used, whatever they hold.
+ * A sequence or position outside the table makes its row see no key, a page
+ *   index outside the cache hides that page's keys; both leave TQ_ERR_VALUE in
+ *   the status word.
+ * Rows may share a sequence (several new tokens of one request, each with its
+ *   own position); each reads the cache for itself.
+ * The keys of a long row are split over the GPU and joined in the same launch,
+ * in a fixed order: repeated calls give identical bits.
+ * q_d and out_d 16-byte aligned.  0 <= m <= 4096; scale finite, window >= 0
+ * (TQ_ERR_VALUE).  Same workspace rules as tq_gemv. */
+TQ_API int tq_attn_workspace(const tq_kv_cache_t* cache, int32_t m, int32_t q_heads, size_t* bytes);
+TQ_API int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_heads, const int32_t* seq_d,
+                   const int32_t* pos_d, float scale, int32_t window, void* out_d, int32_t out_dtype,
+                   void* workspace_d, size_t ws_bytes, void* stream);
+
+/* ---- low-rank adapters beside a projection ----------------------------------------
+ * A trellis-coded weight is frozen; what requests add to it are low-rank
+ * pairs.  For token t with adapter a = adapter_d[t]:
+ *   out[t][n] = y[t][n] + scale[a] * sum_r B[a][n][r] * (sum_k A[a][r][k] x[t][k])
+ * and out[t] = y[t] when a < 0 (no adapter).
+ * a_d: device [n_adapters][rank][k], b_d: device [n_adapters][n][rank], both
+ *   dtype TQ_BF16 or TQ_F16, 16-byte aligned.  scale_d: device fp32
+ *   [n_adapters], or NULL = 1.
+ * rank: a multiple of 8, 8 .. TQ_LORA_MAX_RANK (pad smaller adapters with
+ *   zeros).  k: a positive multiple of 512.  n >= 1. */
+#define TQ_LORA_MAX_RANK 128
+typedef struct tq_lora {
+  const void* a_d;
+  const void* b_d;
+  const float* scale_d;
+  int32_t dtype;
+  int32_t n_adapters, rank, n, k;
+} tq_lora_t;
+
+/* x_d: device [m][k] of the adapters' dtype: the projection's input as the
+ *   adapters were trained on it (bf16 activations, or the fp16 x' of tq_rht
+ *   for adapters of the rotated input), 16-byte aligned.
+ * adapter_d: device int32 [m]; an index >= n_adapters counts as no adapter and
+ *   leaves TQ_ERR_VALUE in the status word.
+ * y_d, out_d: device fp32, row t at t * y_stride / t * out_stride elements
+ *   (>= n), 4-byte aligned (16-byte alignment and strides of a multiple of 4
+ *   are faster), so q, k or v columns of a phase's y can be addressed.  out_d
+ *   may be y_d (then with the same stride); any other overlap is not allowed.
+ * Products are exact, sums are fp32, and A x keeps fp32 accuracy through the
+ * second product.  0 <= m <= 4096 (m == 0: no launch).  Same workspace rules
+ * as tq_gemv. */
+TQ_API int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes);
+TQ_API int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* adapter_d, const float* y_d,
+                   int64_t y_stride, float* out_d, int64_t out_stride, void* workspace_d, size_t ws_bytes,
+                   void* stream);
 
 /* Human-readable text of a status code (static storage). */
 TQ_API const char* tq_status_string(int status);
