@@ -1,4 +1,29 @@
 // tq_attn.cuh -- attention of new tokens over the paged key/value cache.
+//
+// Per row and query head: o = sum_j softmax_j(c q.k_j) v_j over the visible
+// keys, in one pass with the running maximum M and sum L of the softmax
+// (weights 2^(s - M), s = c log2(e) q.k; M rises: O and L are scaled by
+// 2^(M_old - M_new)).
+//
+// Bound: the bytes of the cache, each read once; the query heads that share a
+// key head share its tiles.  A tile is 16 keys of one (row, key head, group of
+// up to 8 or 16 query heads).  All tiles of the call, in row-major order, are
+// split evenly over the blocks and in each block over its warps, whatever the
+// rows' lengths are (the lengths are read on the device, so a captured call
+// serves any).  Each warp streams its tiles through a ring of its own in
+// shared memory (16-byte asynchronous copies; no barrier between warps), and
+// computes
+//   S^T = K Q^T   (m16n8k16: 16 keys x 8 heads)
+//   O^T += V^T P^T  (16 features x 8 heads per MMA)
+// so that the 8-wide side of the MMA is the heads and none of the 16-wide
+// side is padding; P^T's operand layout is the transpose of S^T's result
+// layout (movmatrix).  Warp MMAs suffice: at the cache's bandwidth they need
+// about a tenth of their rate, and the one-row-per-key layout they take needs
+// no tensor map, so any page size and strides work.
+// Items (row, key head, head group) that a warp holds whole are written by
+// it.  The others leave partial (O, M, L): warps of a block join in shared
+// memory, blocks in global memory by the last block to arrive, in block order
+// (the same bits on every run).
 #pragma once
 
 #include "tq_kv.cuh"
@@ -12,72 +37,659 @@ struct AttnParams {
   const int32_t* pos;  // [m]
   void* out;  // [m][q_heads][head_dim]
   int32_t m, q_heads, window;
+  int32_t group;        // query heads per key head
+  int32_t head_groups;  // items per key head
+  int32_t min_tiles;    // tiles a block takes at least before another is used
+  uint32_t page_mul, page_shift;  // j / page_size = (umulhi(j, mul) + j) >> shift
   float scale;
+  int32_t out_bf16;
+  int32_t* counters;
+  float* partials;  // [grid][2][AttnCfg::PART]
   int32_t* status;
 };
 
-template <int T>
-__device__ __forceinline__ float kv_load(const void* p, int64_t i) {
-  if constexpr (T == KV_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  if constexpr (T == KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  if constexpr (T == KV_E4M3) return float(static_cast<const __nv_fp8_e4m3*>(p)[i]);
-  return 0.f;
+template <int T, int D, int NT>
+struct AttnCfg {
+  static constexpr int EB = KvElem<T>::bytes;
+  static constexpr int RB = D * EB;          // bytes of a key
+  static constexpr int CPR = RB / 16;        // 16-byte chunks of a key
+  static constexpr int STRIDE = RB + 16;     // shared-memory row: an odd number of chunks (no bank conflicts)
+  static constexpr int STAGE = 2 * 16 * STRIDE;
+  static constexpr int COLS = 8 * NT;        // head columns
+  static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
+  static constexpr int SLOT = PART * 4;
+  static constexpr int CTL = 2048;
+  static constexpr int fit(int warps) { return ((227 * 1024 - CTL) / warps - SLOT) / STAGE; }
+  // as many warps as leave each a ring of three tiles, else four
+  static constexpr int WARPS = fit(8) >= 3 ? 8 : (fit(6) >= 3 ? 6 : 4);
+  static constexpr int STAGES = fit(WARPS) > 4 ? 4 : fit(WARPS);
+  static constexpr int RING = STAGES * STAGE > SLOT ? STAGES * STAGE : SLOT;  // the tail's partial reuses the ring
+  static constexpr int WARP_BYTES = RING + SLOT;
+  static constexpr int SMEM = WARPS * WARP_BYTES + CTL;
+  static constexpr int THREADS = WARPS * 32;
+  static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && WARP_BYTES % 16 == 0, "ring");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t r[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t lo16) {
+  uint32_t r;
+  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }\n" : "=r"(r) : "r"(lo16));
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    mma_16816(c, a, b0, b1);
 }
 
-// One warp per row and query head: o = sum_j softmax(scale q.k_j) v_j in one
-// pass over the visible keys with the running maximum and sum.
-template <int T, bool OUT_BF16>
-__global__ void __launch_bounds__(128) attn_kernel(AttnParams p) {
-  constexpr int QT = T == KV_BF16 ? KV_BF16 : KV_F16;
+// Where a warp stands in the tile order.
+struct AttnWalk {
+  int64_t row_tile;  // first tile of the row (of the whole call's order)
+  int32_t row, item, j;  // row, item in the row, tile in the item
+  int32_t n;      // tiles of an item of this row (at least one, so that rows without keys are written too)
+  int32_t keys, first, seq;  // visible keys, the first of them, block-table row
+};
+
+__device__ __forceinline__ int32_t attn_keys(const AttnParams& p, int row, int32_t& first, int32_t& seq, bool& bad) {
+  const int32_t pos = p.pos[row];
+  seq = p.seq ? p.seq[row] : row;
+  bad = pos >= 0 && (seq < 0 || seq >= p.c.n_seqs || pos >= p.c.page_size * p.c.max_pages);
+  first = 0;
+  if (pos < 0 || bad) return 0;
+  if (p.window > 0 && pos >= p.window) first = pos - p.window + 1;
+  return pos - first + 1;
+}
+
+__device__ __forceinline__ void attn_row(const AttnParams& p, AttnWalk& w) {
+  bool bad;
+  w.keys = attn_keys(p, w.row, w.first, w.seq, bad);
+  w.n = w.keys > 0 ? (int32_t)(((uint32_t)w.keys + 15u) >> 4) : 1;
+}
+
+__device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int items) {
+  if (++w.j < w.n) return;
+  w.j = 0;
+  if (++w.item < items) return;
+  w.item = 0;
+  w.row_tile += (int64_t)w.n * items;
+  if (++w.row < p.m) attn_row(p, w);
+}
+
+template <int T, int D, int NT>
+__global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = AttnCfg<T, D, NT>;
+  constexpr bool BF = T == KV_BF16;
+  constexpr bool F8 = T == KV_E4M3;
+  constexpr int W = C::WARPS, S = C::STAGES, COLS = C::COLS, MT = D / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  struct Seg {
+    int64_t start;  // first tile of the segment's item
+    int32_t n, row, item;  // n: its tiles, 0 = no segment
+    int32_t pad;
+  };
+  struct Ctl {
+    int64_t warp_sum[W];
+    int64_t row_tile[W];
+    int32_t row[W];
+    Seg seg[W][2];
+    int32_t last;
+  };
+  static_assert(sizeof(Ctl) <= C::CTL, "control block");
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + W * C::WARP_BYTES);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int items = p.c.kv_heads * p.head_groups;
+
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= (int64_t)p.m * p.q_heads) return;
-  const int row = (int)(item / p.q_heads), h = (int)(item % p.q_heads);
-  const int D = p.c.head_dim, per = D / 32;
-  const int kvh = h / (p.q_heads / p.c.kv_heads);
-  const int32_t seq = p.seq ? p.seq[row] : row;
-  int32_t pos = p.pos[row];
-  if (pos >= 0 && (seq < 0 || seq >= p.c.n_seqs || pos / p.c.page_size >= p.c.max_pages)) {
-    if (lane == 0) flag_bad_index(p.status);
-    pos = -1;
+
+  // ---- the split: prefix sums of the rows' tiles -------------------------------
+  const int per = (p.m + C::THREADS - 1) / C::THREADS;
+  const int r0 = tid * per < p.m ? tid * per : p.m;
+  const int r1 = r0 + per < p.m ? r0 + per : p.m;
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    AttnWalk w;
+    bool bad;
+    const int32_t keys = attn_keys(p, r, w.first, w.seq, bad);
+    if (bad && blockIdx.x == 0) flag_bad_index(p.status);
+    mine += keys > 0 ? (((uint32_t)keys + 15u) >> 4) : 1;
   }
-  const int32_t first = p.window > 0 && pos + 1 > p.window ? pos + 1 - p.window : 0;
-  float q[8], o[8];
-  for (int i = 0; i < 8; ++i) {
-    q[i] = i < per ? kv_load<QT>(p.q, item * D + i * 32 + lane) : 0.f;
-    o[i] = 0.f;
+  int64_t incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
   }
-  const float ks = p.c.ks ? p.c.ks[kvh] : 1.f, vs = p.c.vs ? p.c.vs[kvh] : 1.f;
-  float mx = -INFINITY, sum = 0.f;
-  for (int32_t j = first; j <= pos; ++j) {
-    const int32_t pi = j / p.c.page_size;
-    const int32_t page = p.c.pages[(int64_t)seq * p.c.max_pages + pi];
-    if (page < 0 || page >= p.c.n_pages) {
-      if (lane == 0) flag_bad_index(p.status);
+  if (lane == 31) ctl->warp_sum[warp] = incl;
+  if (tid < W * 2) ctl->seg[tid >> 1][tid & 1].n = 0;
+  __syncthreads();
+  int64_t before = 0, rows_total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (i < warp) before += ctl->warp_sum[i];
+    rows_total += ctl->warp_sum[i];
+  }
+  const int64_t total = rows_total * items;
+  int64_t blocks = (total + p.min_tiles - 1) / p.min_tiles;
+  if (blocks > gridDim.x) blocks = gridDim.x;
+  if (blockIdx.x >= blocks) return;
+  const int64_t b0 = total * blockIdx.x / blocks, b1 = total * (blockIdx.x + 1) / blocks;
+  {
+    int64_t at = (before + incl - mine) * items;  // first tile of row r0
+    const int64_t end = (before + incl) * items;
+    if (end > b0 && at < b1) {
+      for (int r = r0; r < r1; ++r) {
+        AttnWalk w;
+        w.row = r;
+        attn_row(p, w);
+        const int64_t nx = at + (int64_t)w.n * items;
+        for (int i = 0; i < W; ++i) {
+          const int64_t s = b0 + (b1 - b0) * i / W;
+          if (s >= at && s < nx) {
+            ctl->row[i] = r;
+            ctl->row_tile[i] = at;
+          }
+        }
+        at = nx;
+      }
+    }
+  }
+  __syncthreads();
+  const int64_t w0 = b0 + (b1 - b0) * warp / W, w1 = b0 + (b1 - b0) * (warp + 1) / W;
+  int64_t left = w1 - w0;  // tiles of this warp
+
+  uint8_t* ring = smem + warp * C::WARP_BYTES;
+  float* head_slot = reinterpret_cast<float*>(ring + C::RING);  // O of the first item when it began before the warp
+  float* tail_slot = reinterpret_cast<float*>(ring);            // O of the last item when it goes on (ring drained)
+  const uint32_t ring_u = smem_u32(ring);
+
+  if (left > 0) {
+    AttnWalk cw;  // consumer
+    cw.row = ctl->row[warp];
+    cw.row_tile = ctl->row_tile[warp];
+    attn_row(p, cw);
+    {
+      const int64_t o = w0 - cw.row_tile;
+      cw.item = (int32_t)(o / cw.n);
+      cw.j = (int32_t)(o - (int64_t)cw.item * cw.n);
+    }
+    AttnWalk pw = cw;  // producer: the tile whose pages are looked up next
+    int64_t to_look = left;
+
+    // look-up state of the producer: lane l < 16 holds key l of the tile
+    int32_t page = 0;
+    int64_t off = 0;  // offset inside the page, head included
+    bool valid = false;
+    auto look = [&]() {
+      valid = false;
+      if (to_look > 0) {
+        const int32_t idx = (pw.j << 4) + (lane & 15);
+        if (idx < pw.keys) {
+          const uint32_t t = (uint32_t)(pw.first + idx);
+          const uint32_t pi = (__umulhi(t, p.page_mul) + t) >> p.page_shift;
+          page = p.c.pages[(int64_t)pw.seq * p.c.max_pages + pi];
+          off = (int64_t)(t - pi * (uint32_t)p.c.page_size) * p.c.token_stride +
+                (int64_t)(pw.item / p.head_groups) * p.c.head_stride;
+          valid = true;
+        }
+        --to_look;
+        if (to_look > 0) attn_next(p, pw, items);
+      }
+    };
+    uint64_t masks = 0;  // valid keys of the tiles in flight, 16 bits each, the oldest highest
+    int stage_in = 0;
+    auto copy = [&]() {  // start the copies of the looked-up tile
+      bool ok = valid;
+      if (ok && (page < 0 || page >= p.c.n_pages)) {
+        flag_bad_index(p.status);
+        ok = false;
+      }
+      const int64_t o = ok ? (int64_t)page * p.c.page_stride + off : -1;
+      const uint32_t vm = __ballot_sync(0xffffffffu, ok) & 0xffffu;
+      masks = (masks << 16) | vm;
+      if (vm) {
+        const uint32_t base = ring_u + stage_in * C::STAGE;
+#pragma unroll
+        for (int i = 0; i < C::CPR / 2; ++i) {
+          const int c = i * 32 + lane;
+          const int r = c / C::CPR, ch = c - r * C::CPR;
+          const int64_t ro = __shfl_sync(0xffffffffu, o, r);
+          const int64_t bo = (ro < 0 ? 0 : ro) * C::EB + ch * 16;
+          const uint32_t d = base + r * C::STRIDE + ch * 16;
+          cp_async16(d, static_cast<const uint8_t*>(p.c.k) + (ro < 0 ? 0 : bo), ro >= 0);
+          cp_async16(d + 16 * C::STRIDE, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
+        }
+      }
+      cp_async_commit();
+      if (++stage_in == S) stage_in = 0;
+    };
+
+    look();
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      copy();
+      look();
+    }
+
+    uint32_t qf[NT][MT][2];
+    float o[MT][NT][4];
+    float mx[NT][2], sum[NT][2];
+    float sc = 0.f, vscale = 1.f;
+    bool fresh = true;       // load the item's queries before the next tile
+    bool began_before = cw.j > 0;
+    int stage_out = 0;
+
+    // this lane's query column and the address of its fragment elements
+    auto head_of = [&](int item, int col) {  // query head of a column, or -1
+      const int kvh = item / p.head_groups, hg = item - kvh * p.head_groups;
+      const int g = hg * COLS + col;
+      return g < p.group ? kvh * p.group + g : -1;
+    };
+
+    for (; left > 0; --left) {
+      if (fresh) {
+        fresh = false;
+        const int kvh = cw.item / p.head_groups;
+        sc = p.scale * 1.44269504088896340736f * (p.c.ks ? p.c.ks[kvh] : 1.f);
+        vscale = p.c.vs ? p.c.vs[kvh] : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int h = head_of(cw.item, nt * 8 + (lane >> 2));
+          const uint16_t* qp = static_cast<const uint16_t*>(p.q) + ((int64_t)cw.row * p.q_heads + (h < 0 ? 0 : h)) * D;
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks) {
+            uint32_t x0 = 0, x1 = 0;
+            if (h >= 0) {
+              if constexpr (F8) {  // k slots 2q.. and 2q+8.. of a step hold features 4q.. and 4q+2..
+                const uint2 v = *reinterpret_cast<const uint2*>(qp + ks * 16 + (lane & 3) * 4);
+                x0 = v.x;
+                x1 = v.y;
+              } else {
+                x0 = *reinterpret_cast<const uint32_t*>(qp + ks * 16 + (lane & 3) * 2);
+                x1 = *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8 + (lane & 3) * 2);
+              }
+            }
+            qf[nt][ks][0] = x0;
+            qf[nt][ks][1] = x1;
+          }
+          mx[nt][0] = mx[nt][1] = -INFINITY;
+          sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
+        }
+      }
+
+      cp_async_wait<S - 2>();
+      __syncwarp();
+      const uint32_t vm = (uint32_t)(masks >> (16 * (S - 2))) & 0xffffu;
+      copy();  // into the stage that the previous tile has left
+      look();
+
+      if (vm) {
+        const uint32_t kb = ring_u + stage_out * C::STAGE;
+        const uint32_t vb = kb + 16 * C::STRIDE;
+        // S^T
+        float s[NT][4], s2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
+        const uint32_t ka = kb + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::STRIDE + (lane >> 4) * 16;
+        if constexpr (!F8) {
+#pragma unroll
+          for (int ks = 0; ks < MT; ++ks) {
+            uint32_t a[4];
+            ldsm4(a, ka + ks * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16<BF>((ks & 1) ? s2[nt] : s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+          }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < MT; ks += 2) {
+            uint32_t r[4];
+            ldsm4(r, ka + ks * 16);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t a[4] = {e4m3x2_to_h2(r[2 * u]), e4m3x2_to_h2(r[2 * u + 1]), e4m3x2_to_h2(r[2 * u] >> 16),
+                                     e4m3x2_to_h2(r[2 * u + 1] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16<BF>(u ? s2[nt] : s[nt], a, qf[nt][ks + u][0], qf[nt][ks + u][1]);
+            }
+          }
+        }
+        // softmax: lane holds keys lane/4 and lane/4 + 8 of heads 2(lane%4) and +1
+        const bool v0 = (vm >> (lane >> 2)) & 1, v1 = (vm >> ((lane >> 2) + 8)) & 1;
+        float tm[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s[nt][i] = v0 ? (s[nt][i] + s2[nt][i]) * sc : -INFINITY;
+            s[nt][i + 2] = v1 ? (s[nt][i + 2] + s2[nt][i + 2]) * sc : -INFINITY;
+            tm[nt][i] = fmaxf(s[nt][i], s[nt][i + 2]);
+          }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tm[nt][i] = fmaxf(tm[nt][i], __shfl_xor_sync(0xffffffffu, tm[nt][i], d));
+        bool up = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) up |= tm[nt][i] > mx[nt][i];
+        if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float mn = fmaxf(mx[nt][i], tm[nt][i]);
+              const float f = mn == -INFINITY ? 1.f : ex2(mx[nt][i] - mn);
+              mx[nt][i] = mn;
+              sum[nt][i] *= f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                o[mt][nt][i] *= f;
+                o[mt][nt][i + 2] *= f;
+              }
+            }
+        }
+        // P^T as the B operand.  fp16 weights are rounded to 2^-12 (e4m3 and
+        // fp16 caches; at most 1, exact for a key that takes all); bf16
+        // caches need bf16 weights, whose 2^-9 would be felt in the output,
+        // so they go in as two terms (2^-17) and two MMAs.
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float e[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float m0 = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
+              e[i] = ex2(s[nt][2 * r + i] - m0);
+              sum[nt][i] += e[i];
+            }
+            if constexpr (BF) {
+              const uint32_t h = KvElem<KV_BF16>::pack2(e[0], e[1]);
+              const uint32_t l = KvElem<KV_BF16>::pack2(e[0] - __uint_as_float(h << 16), e[1] - __uint_as_float(h & 0xffff0000u));
+              ph[nt][r] = transpose8(h);
+              pl[nt][r] = transpose8(l);
+            } else {
+              ph[nt][r] = transpose8(f2_to_h2(e[0], e[1]));
+            }
+          }
+        }
+        // O^T
+        if constexpr (!F8) {
+          const uint32_t va = vb + ((lane & 7) + (lane >> 4) * 8) * C::STRIDE + ((lane >> 3) & 1) * 16;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            ldsm4_t(a, va + mt * 32);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma16<BF>(o[mt][nt], a, ph[nt][0], ph[nt][1]);
+              if constexpr (BF) mma16<BF>(o[mt][nt], a, pl[nt][0], pl[nt][1]);
+            }
+          }
+        } else {
+          // a 16-bit element of the transposed load is a pair of neighbouring
+          // features: MMA rows r and r + 8 are features 2r and 2r + 1
+          const uint32_t va = vb + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::STRIDE + (lane >> 4) * 16;
+#pragma unroll
+          for (int mt = 0; mt < MT; mt += 2) {
+            uint32_t r[4];
+            ldsm4_t(r, va + mt * 16);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t x = __byte_perm(r[2 * u], 0, 0x3120), y = __byte_perm(r[2 * u + 1], 0, 0x3120);
+              const uint32_t a[4] = {e4m3x2_to_h2(x), e4m3x2_to_h2(x >> 16), e4m3x2_to_h2(y), e4m3x2_to_h2(y >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, ph[nt][0], ph[nt][1]);
+            }
+          }
+        }
+      }
+      if (++stage_out == S) stage_out = 0;
+      __syncwarp();
+
+      // ---- end of the item or of the warp's range ---------------------------------
+      const bool item_end = cw.j + 1 == cw.n;
+      if (item_end || left == 1) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sum[nt][i] += __shfl_xor_sync(0xffffffffu, sum[nt][i], d);
+        if (item_end && !began_before) {
+          // whole item: normalise, round, transpose to [head][feature], write
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float inv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) inv[i] = sum[nt][i] == 0.f ? 0.f : vscale / sum[nt][i];
+            const int h = head_of(cw.item, nt * 8 + (lane >> 2));
+            uint16_t* op = static_cast<uint16_t*>(p.out) + ((int64_t)cw.row * p.q_heads + (h < 0 ? 0 : h)) * D;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const float* v = o[mt][nt];
+              const float y0 = v[0] * inv[0], y1 = v[1] * inv[1], y2 = v[2] * inv[0], y3 = v[3] * inv[1];
+              const uint32_t t0 = transpose8(p.out_bf16 ? KvElem<KV_BF16>::pack2(y0, y1) : f2_to_h2(y0, y1));
+              const uint32_t t1 = transpose8(p.out_bf16 ? KvElem<KV_BF16>::pack2(y2, y3) : f2_to_h2(y2, y3));
+              if (h >= 0) {
+                if constexpr (F8) {  // t0: features 4q, 4q+2; t1: 4q+1, 4q+3
+                  *reinterpret_cast<uint2*>(op + mt * 16 + (lane & 3) * 4) =
+                      make_uint2(__byte_perm(t0, t1, 0x5410), __byte_perm(t0, t1, 0x7632));
+                } else {
+                  *reinterpret_cast<uint32_t*>(op + mt * 16 + (lane & 3) * 2) = t0;
+                  *reinterpret_cast<uint32_t*>(op + mt * 16 + 8 + (lane & 3) * 2) = t1;
+                }
+              }
+            }
+          }
+        } else {
+          const int slot = item_end ? 0 : 1;
+          if (!item_end) {
+            cp_async_wait<0>();  // the ring is empty before its bytes are reused
+            __syncwarp();
+          }
+          float* dst = item_end ? head_slot : tail_slot;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int d0 = F8 ? mt * 16 + 2 * (lane >> 2) : mt * 16 + (lane >> 2);
+            const int d1 = F8 ? d0 + 1 : d0 + 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int col = nt * 8 + (lane & 3) * 2;
+              *reinterpret_cast<float2*>(dst + d0 * COLS + col) = make_float2(o[mt][nt][0], o[mt][nt][1]);
+              *reinterpret_cast<float2*>(dst + d1 * COLS + col) = make_float2(o[mt][nt][2], o[mt][nt][3]);
+            }
+          }
+          if (lane < 4) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int col = nt * 8 + lane * 2 + i;
+                dst[D * COLS + col] = mx[nt][i];
+                dst[D * COLS + COLS + col] = sum[nt][i];
+              }
+          }
+          if (lane == 0) {
+            Seg& g = ctl->seg[warp][slot];
+            g.start = cw.row_tile + (int64_t)cw.item * cw.n;
+            g.n = cw.n;
+            g.row = cw.row;
+            g.item = cw.item;
+          }
+        }
+        began_before = false;
+        fresh = true;
+      }
+      attn_next(p, cw, items);
+    }
+    cp_async_wait<0>();
+  }
+  __syncthreads();
+
+  // ---- join: first the block's warps, then the blocks of an item ----------------
+  auto slot_ptr = [&](int i) {  // i = 2 warp + slot
+    uint8_t* b = smem + (i >> 1) * C::WARP_BYTES;
+    return reinterpret_cast<const float*>((i & 1) ? b : b + C::RING);
+  };
+  auto block_of = [&](int64_t tile) { return (int)(((tile + 1) * blocks - 1) / total); };
+  constexpr int QUADS = D * COLS / 4;  // float4 of an O
+  constexpr int QPT = (QUADS + C::THREADS - 1) / C::THREADS;
+  for (int i = 0; i < 2 * W;) {
+    const Seg g = ctl->seg[i >> 1][i & 1];
+    if (g.n == 0) {
+      ++i;
       continue;
     }
-    const int64_t off = (int64_t)page * p.c.page_stride + (int64_t)(j - pi * p.c.page_size) * p.c.token_stride +
-                        (int64_t)kvh * p.c.head_stride;
-    float s = 0.f;
-    for (int i = 0; i < per; ++i) s += q[i] * kv_load<T>(p.c.k, off + i * 32 + lane);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale * ks;
-    const float mn = fmaxf(mx, s);
-    const float corr = mx == -INFINITY ? 0.f : expf(mx - mn);
-    const float e = expf(s - mn);
-    sum = sum * corr + e;
-    for (int i = 0; i < per; ++i) o[i] = o[i] * corr + e * kv_load<T>(p.c.v, off + i * 32 + lane);
-    mx = mn;
-  }
-  const float inv = sum > 0.f ? vs / sum : (sum == sum ? 0.f : sum);
-  for (int i = 0; i < per; ++i) {
-    const int64_t at = item * D + i * 32 + lane;
-    if constexpr (OUT_BF16)
-      static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(o[i] * inv);
-    else
-      static_cast<__half*>(p.out)[at] = __float2half_rn(o[i] * inv);
+    int e = i + 1;  // segments [i, e) are of this item
+    while (e < 2 * W) {
+      const Seg& x = ctl->seg[e >> 1][e & 1];
+      if (x.n != 0 && x.start != g.start) break;
+      ++e;
+    }
+    const int c_first = block_of(g.start), c_last = block_of(g.start + g.n - 1);
+    const bool whole = c_first == c_last;
+    float* gp = p.partials + ((int64_t)blockIdx.x * 2 + (c_first == (int)blockIdx.x ? 1 : 0)) * C::PART;
+    float4 acc[QPT];
+    float M[4], L[4];
+    const int col = (tid * 4) % COLS;  // the same for all of a thread's quads (THREADS * 4 is a multiple of COLS)
+    // weights of each part from its M: sum_i 2^(M_i - M) O_i, and so for L
+    auto maxima = [&](const float* part) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) M[k] = fmaxf(M[k], part[D * COLS + col + k]);
+    };
+    auto add = [&](const float* part) {
+      float f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k] = M[k] == -INFINITY ? 0.f : ex2(part[D * COLS + col + k] - M[k]);
+        L[k] += f[k] * part[D * COLS + COLS + col + k];
+      }
+#pragma unroll
+      for (int u = 0; u < QPT; ++u) {
+        const int qd = u * C::THREADS + tid;
+        if (QUADS % C::THREADS == 0 || qd < QUADS) {
+          const float4 v = *reinterpret_cast<const float4*>(part + qd * 4);
+          acc[u].x += f[0] * v.x;
+          acc[u].y += f[1] * v.y;
+          acc[u].z += f[2] * v.z;
+          acc[u].w += f[3] * v.w;
+        }
+      }
+    };
+    auto clear = [&]() {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        M[k] = -INFINITY;
+        L[k] = 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    auto write = [&]() {
+      const int kvh = g.item / p.head_groups, hg = g.item - kvh * p.head_groups;
+      const float vsc = p.c.vs ? p.c.vs[kvh] : 1.f;
+#pragma unroll
+      for (int u = 0; u < QPT; ++u) {
+        const int qd = u * C::THREADS + tid;
+        if (QUADS % C::THREADS != 0 && qd >= QUADS) continue;
+        const int d = qd * 4 / COLS;
+        const float v[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int gh = hg * COLS + col + k;
+          if (gh >= p.group) continue;
+          const float y = L[k] == 0.f ? 0.f : v[k] * (vsc / L[k]);
+          const int64_t at = ((int64_t)g.row * p.q_heads + kvh * p.group + gh) * D + d;
+          if (p.out_bf16)
+            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
+          else
+            static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+        }
+      }
+    };
+    clear();
+    for (int k = i; k < e; ++k)
+      if (ctl->seg[k >> 1][k & 1].n) maxima(slot_ptr(k));
+    for (int k = i; k < e; ++k)
+      if (ctl->seg[k >> 1][k & 1].n) add(slot_ptr(k));
+    if (whole) {
+      write();
+    } else {
+#pragma unroll
+      for (int u = 0; u < QPT; ++u) {
+        const int qd = u * C::THREADS + tid;
+        if (QUADS % C::THREADS == 0 || qd < QUADS) *reinterpret_cast<float4*>(gp + qd * 4) = acc[u];
+      }
+      if (tid < COLS / 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          gp[D * COLS + col + k] = M[k];
+          gp[D * COLS + COLS + col + k] = L[k];
+        }
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) ctl->last = atomicAdd(p.counters + c_first, 1) == c_last - c_first;
+      __syncthreads();
+      if (ctl->last) {
+        __threadfence();
+        clear();
+        const float* pp = p.partials;
+        for (int c = c_first; c <= c_last; ++c) maxima(pp + ((int64_t)c * 2 + (c == c_first)) * C::PART);
+#pragma unroll 4
+        for (int c = c_first; c <= c_last; ++c) add(pp + ((int64_t)c * 2 + (c == c_first)) * C::PART);
+        write();
+        if (tid == 0) p.counters[c_first] = 0;
+      }
+      __syncthreads();
+    }
+    i = e;
   }
 }
 

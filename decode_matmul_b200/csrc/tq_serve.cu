@@ -69,9 +69,54 @@ int check_ws(const void* ws, size_t have, size_t need) {
   return TQ_OK;
 }
 
-size_t attn_ws_bytes(const tq_kv_cache_t* c, int32_t m, int32_t q_heads) {
-  (void)c, (void)m, (void)q_heads;
-  return kCounterBytes;
+// Attention: one block per SM; two partial results per block.
+constexpr int kAttnMaxBlocks = 148;
+constexpr int kAttnMinTiles = 8;  // tiles of 16 keys a block takes before another is used
+
+int attn_cols(const tq_kv_cache_t* c, int32_t q_heads) { return q_heads / c->kv_heads <= 8 ? 8 : 16; }
+
+size_t attn_ws_bytes(const tq_kv_cache_t* c, int32_t q_heads) {
+  const int cols = attn_cols(c, q_heads);
+  return kCounterBytes + (size_t)kAttnMaxBlocks * 2 * (c->head_dim * cols + 2 * cols) * sizeof(float);
+}
+
+// Multiplier and shift of an exact division of values below 2^31 by d:
+// n / d = (umulhi(n, mul) + n) >> shift (Granlund and Montgomery 1994).
+void divider(uint32_t d, uint32_t* mul, uint32_t* shift) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  *mul = (uint32_t)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+  *shift = l;
+}
+
+template <int T, int D, int NT>
+int attn_launch(const tq::AttnParams& p, int sms, cudaStream_t stream) {
+  using C = tq::AttnCfg<T, D, NT>;
+  auto kern = tq::attn_kernel<T, D, NT>;
+  static int configured[kMaxDevices];
+  int dev = 0;
+  TQ_CUDA(cudaGetDevice(&dev));
+  if (!configured[dev]) {
+    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
+    configured[dev] = 1;
+  }
+  const int grid = sms < kAttnMaxBlocks ? sms : kAttnMaxBlocks;
+  return launch(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, p);
+}
+
+template <int T, int D>
+int attn_launch_d(const tq::AttnParams& p, int cols, int sms, cudaStream_t stream) {
+  return cols == 8 ? attn_launch<T, D, 1>(p, sms, stream) : attn_launch<T, D, 2>(p, sms, stream);
+}
+
+template <int T>
+int attn_launch_t(const tq::AttnParams& p, int cols, int sms, cudaStream_t stream) {
+  switch (p.c.head_dim) {
+    case 64: return attn_launch_d<T, 64>(p, cols, sms, stream);
+    case 96: return attn_launch_d<T, 96>(p, cols, sms, stream);
+    case 128: return attn_launch_d<T, 128>(p, cols, sms, stream);
+    default: return attn_launch_d<T, 256>(p, cols, sms, stream);
+  }
 }
 
 int check_lora(const tq_lora_t* l) {
@@ -146,7 +191,7 @@ int tq_attn_workspace(const tq_kv_cache_t* cache, int32_t m, int32_t q_heads, si
   if (st != TQ_OK) return st;
   st = check_heads(cache, m, q_heads);
   if (st != TQ_OK) return st;
-  *bytes = attn_ws_bytes(cache, m, q_heads);
+  *bytes = attn_ws_bytes(cache, q_heads);
   return TQ_OK;
 }
 
@@ -162,7 +207,7 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   if (m == 0) return TQ_OK;
   if (!q_d || !pos_d || !out_d) return TQ_ERR_NULL;
   if (!aligned16(q_d) || !aligned16(out_d) || !aligned_to(pos_d, 4) || !aligned_to(seq_d, 4)) return TQ_ERR_ALIGN;
-  st = check_ws(workspace_d, ws_bytes, attn_ws_bytes(cache, m, q_heads));
+  st = check_ws(workspace_d, ws_bytes, attn_ws_bytes(cache, q_heads));
   if (st != TQ_OK) return st;
   int sms = 0;
   st = check_arch(&sms);
@@ -177,21 +222,20 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   p.q_heads = q_heads;
   p.window = window;
   p.scale = scale;
+  p.group = q_heads / cache->kv_heads;
+  const int cols = attn_cols(cache, q_heads);
+  p.head_groups = (p.group + cols - 1) / cols;
+  p.min_tiles = kAttnMinTiles;
+  divider((uint32_t)cache->page_size, &p.page_mul, &p.page_shift);
+  p.out_bf16 = out_dtype == TQ_BF16;
+  p.counters = static_cast<int32_t*>(workspace_d);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + kCounterBytes);
   p.status = status_word(workspace_d);
-  const int64_t items = (int64_t)m * q_heads;
-  const dim3 grid((unsigned)((items + 3) / 4)), block(128);
   cudaStream_t s = (cudaStream_t)stream;
-  const bool bf = out_dtype == TQ_BF16;
   switch (cache->dtype) {
-    case TQ_F16:
-      return bf ? launch(tq::attn_kernel<tq::KV_F16, true>, grid, block, 0, s, p)
-                : launch(tq::attn_kernel<tq::KV_F16, false>, grid, block, 0, s, p);
-    case TQ_BF16:
-      return bf ? launch(tq::attn_kernel<tq::KV_BF16, true>, grid, block, 0, s, p)
-                : launch(tq::attn_kernel<tq::KV_BF16, false>, grid, block, 0, s, p);
-    default:
-      return bf ? launch(tq::attn_kernel<tq::KV_E4M3, true>, grid, block, 0, s, p)
-                : launch(tq::attn_kernel<tq::KV_E4M3, false>, grid, block, 0, s, p);
+    case TQ_F16: return attn_launch_t<tq::KV_F16>(p, cols, sms, s);
+    case TQ_BF16: return attn_launch_t<tq::KV_BF16>(p, cols, sms, s);
+    default: return attn_launch_t<tq::KV_E4M3>(p, cols, sms, s);
   }
 }
 
