@@ -8,6 +8,7 @@ raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -388,6 +389,10 @@ def tq_ldlq_encode(w_rot, u, codebook, gain: float, refits: int = 1, codes=None,
 
 # ---- attention between the phases, adapters beside a projection --------------------
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _code(dtype) -> int:
     """TQ_* code of a torch dtype (None: not a type of these calls)."""
     import torch
@@ -396,39 +401,35 @@ def _code(dtype) -> int:
 
 def _need(t, name: str, dtype, shape, device):
     """A contiguous tensor of this type, shape and device (ValueError otherwise)."""
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)} on {device} is needed, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else " (strided)"))
 
 
-def _need_ws(ws, device):
+def _on(device, stream):
+    """Context in which the tensors' device is current, and the given stream too (so that what a call allocates
+    belongs to the stream it runs on)."""
     import torch
-    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+    if device.type != "cuda":
+        raise ValueError(f"a CUDA tensor is needed, got {device}")
+    if stream is None:
+        return _AS_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)  # makes the stream's device current as well
+
+
+_AS_IS = contextlib.nullcontext()
+
+
+def _workspace_ptr(ws, nbytes: int, device):
+    """Address and size of the workspace, `ws` or (None) a new one, which the caller keeps until its launch."""
+    import torch
+    if ws is None:
+        ws = workspace(nbytes, device)
+    elif ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
         raise ValueError(f"ws: a contiguous uint8 tensor on {device} is needed")
-
-
-class _on:
-    """Make the tensors' device current, and the given stream too (so that what a call allocates belongs to the
-    stream it runs on)."""
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError(f"a CUDA tensor is needed, got {device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.dev = torch.cuda.device(device)
-        self.stream = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self.dev.__enter__()
-        self.stream.__enter__()
-
-    def __exit__(self, *a):
-        self.stream.__exit__(*a)
-        self.dev.__exit__(*a)
+    return ws
 
 
 class KvCache:
@@ -452,8 +453,9 @@ class KvCache:
         if pages.dim() != 2:
             raise ValueError("pages: an int32 [n_seqs][max_pages] tensor is needed")
         _need(pages, "pages", torch.int32, pages.shape, k.device)
-        _need(k_scale, "k_scale", torch.float32, (k.shape[2],), k.device)
-        _need(v_scale, "v_scale", torch.float32, (k.shape[2],), k.device)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _need(t, name, torch.float32, (k.shape[2],), k.device)
         self.k, self.v, self.pages, self.k_scale, self.v_scale = k, v, pages, k_scale, v_scale
         self.device = k.device
         self.kv_heads, self.head_dim = k.shape[2], k.shape[3]
@@ -462,6 +464,7 @@ class KvCache:
                                      None if k_scale is None else k_scale.data_ptr(),
                                      None if v_scale is None else v_scale.data_ptr(), *strides[0], _code(k.dtype),
                                      k.shape[0], k.shape[1], k.shape[2], k.shape[3], pages.shape[0], pages.shape[1])
+        self._ref = ctypes.byref(self._struct)
 
     def struct(self) -> tq_kv_cache_t:
         return self._struct
@@ -477,12 +480,14 @@ class Lora:
             raise ValueError("a [n_adapters][rank][k] and b [n_adapters][n][rank] of float16 or bfloat16 are needed")
         _need(a, "a", a.dtype, a.shape, a.device)
         _need(b, "b", a.dtype, (a.shape[0], b.shape[1], a.shape[1]), a.device)
-        _need(scale, "scale", torch.float32, (a.shape[0],), a.device)
+        if scale is not None:
+            _need(scale, "scale", torch.float32, (a.shape[0],), a.device)
         self.a, self.b, self.scale, self.device = a, b, scale, a.device
         self.n_adapters, self.rank, self.k = a.shape
         self.n = b.shape[1]
         self._struct = tq_lora_t(a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr(),
                                  _code(a.dtype), self.n_adapters, self.rank, self.n, self.k)
+        self._ref = ctypes.byref(self._struct)
 
     def struct(self) -> tq_lora_t:
         return self._struct
@@ -501,28 +506,29 @@ def tq_kv_append(cache: KvCache, qkv, q_heads: int, pos, freq=None, interleaved:
     rows of the block table (None: token t is sequence t).  Returns the rotated queries [m][q_heads][head_dim]
     (bfloat16 for a bfloat16 cache, else float16)."""
     import torch
-    dev, m = cache.device, qkv.shape[0]
-    if (qkv.dim() != 2 or qkv.dtype != torch.float32 or qkv.device != dev or qkv.stride(1) != 1
-            or qkv.shape[1] != (q_heads + 2 * cache.kv_heads) * cache.head_dim):
-        raise ValueError(f"qkv: float32 rows of {q_heads} + 2 x {cache.kv_heads} heads of {cache.head_dim} on {dev} are "
-                         "needed")
+    dev, m, D = cache.device, qkv.shape[0], cache.head_dim
+    width = (q_heads + 2 * cache.kv_heads) * D
+    if (qkv.dtype is not torch.float32 or qkv.shape != (m, width) or qkv.device != dev or qkv.stride(1) != 1):
+        raise ValueError(f"qkv: float32 rows of {q_heads} + 2 x {cache.kv_heads} heads of {D} on {dev} are needed")
     _need(pos, "pos", torch.int32, (m,), dev)
-    _need(seq, "seq", torch.int32, (m,), dev)
-    half = 0 if freq is None else freq.numel()
-    _need(freq, "freq", torch.float64, (half,), dev)
-    _need(q_out, "q_out", cache.q_dtype, (m, q_heads, cache.head_dim), dev)
-    if seq is None and m > cache.pages.shape[0]:
+    if seq is not None:
+        _need(seq, "seq", torch.int32, (m,), dev)
+    elif m > cache.pages.shape[0]:
         raise ValueError(f"{m} tokens without seq, but the block table has {cache.pages.shape[0]} rows")
+    half = 0
+    if freq is not None:
+        half = freq.numel()
+        _need(freq, "freq", torch.float64, (half,), dev)
+    if q_out is not None:
+        _need(q_out, "q_out", cache.q_dtype, (m, q_heads, D), dev)
     with _on(dev, stream):
         if q_out is None:
-            q_out = torch.empty((m, q_heads, cache.head_dim), dtype=cache.q_dtype, device=dev)
-        if ws is None:
-            ws = workspace(tq_kv_append_workspace(), dev)
-        _need_ws(ws, dev)
-        row = qkv.shape[1] if m == 1 else qkv.stride(0)
-        _ok(_lib().tq_kv_append(ctypes.byref(cache.struct()), _ptr(qkv), row, m, q_heads, _ptr(seq), _ptr(pos),
-                                _ptr(freq), 2 * half, int(bool(interleaved)), _ptr(q_out), _ptr(ws), ws.numel(),
-                                _stream()), "tq_kv_append")
+            q_out = torch.empty((m, q_heads, D), dtype=cache.q_dtype, device=dev)
+        ws = _workspace_ptr(ws, 65536, dev)
+        st = _lib().tq_kv_append(cache._ref, qkv.data_ptr(), width if m == 1 else qkv.stride(0), m, q_heads, _addr(seq),
+                                 pos.data_ptr(), _addr(freq), 2 * half, 1 if interleaved else 0, q_out.data_ptr(),
+                                 ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    _ok(st, "tq_kv_append")
     return q_out
 
 
@@ -541,23 +547,23 @@ def tq_attn(cache: KvCache, q, pos, scale: float, seq=None, window: int = 0, out
     dev = cache.device
     if q.dim() != 3:
         raise ValueError("q: [m][q_heads][head_dim] is needed")
-    m, q_heads = q.shape[:2]
+    m, q_heads, _ = q.shape
     _need(q, "q", cache.q_dtype, (m, q_heads, cache.head_dim), dev)
     _need(pos, "pos", torch.int32, (m,), dev)
-    _need(seq, "seq", torch.int32, (m,), dev)
-    if seq is None and m > cache.pages.shape[0]:
+    if seq is not None:
+        _need(seq, "seq", torch.int32, (m,), dev)
+    elif m > cache.pages.shape[0]:
         raise ValueError(f"{m} rows without seq, but the block table has {cache.pages.shape[0]} rows")
     if out is not None:
-        _need(out, "out", torch.float16 if out.dtype == torch.float16 else torch.bfloat16, q.shape, dev)
-        out_dtype = _code(out.dtype)
+        out_dtype = TQ_F16 if out.dtype is torch.float16 else TQ_BF16
+        _need(out, "out", torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, q.shape, dev)
     with _on(dev, stream):
         if out is None:
             out = torch.empty(q.shape, dtype=torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, device=dev)
-        if ws is None:
-            ws = workspace(tq_attn_workspace(cache, m, q_heads), dev)
-        _need_ws(ws, dev)
-        _ok(_lib().tq_attn(ctypes.byref(cache.struct()), _ptr(q), m, q_heads, _ptr(seq), _ptr(pos), float(scale),
-                           int(window), _ptr(out), out_dtype, _ptr(ws), ws.numel(), _stream()), "tq_attn")
+        ws = _workspace_ptr(ws, 0 if ws is not None else tq_attn_workspace(cache, m, q_heads), dev)
+        st = _lib().tq_attn(cache._ref, q.data_ptr(), m, q_heads, _addr(seq), pos.data_ptr(), scale, window,
+                            out.data_ptr(), out_dtype, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    _ok(st, "tq_attn")
     return out
 
 
@@ -576,14 +582,13 @@ def tq_lora(lora: Lora, x, adapter, y, out=None, ws=None, stream=None):
     _need(adapter, "adapter", torch.int32, (m,), dev)
     out = y if out is None else out
     for name, t in (("y", y), ("out", out)):
-        if t.dtype != torch.float32 or tuple(t.shape) != (m, lora.n) or t.device != dev or (
-                t.numel() and lora.n > 1 and t.stride(1) != 1):
+        if t.dtype is not torch.float32 or t.shape != (m, lora.n) or t.device != dev or (
+                lora.n > 1 and m > 0 and t.stride(1) != 1):
             raise ValueError(f"{name}: float32 [{m}][{lora.n}] with contiguous rows on {dev} is needed")
     with _on(dev, stream):
-        if ws is None:
-            ws = workspace(tq_lora_workspace(lora, m), dev)
-        _need_ws(ws, dev)
-        ys, os_ = (lora.n if m <= 1 else t.stride(0) for t in (y, out))
-        _ok(_lib().tq_lora(ctypes.byref(lora.struct()), _ptr(x), m, _ptr(adapter), _ptr(y), ys, _ptr(out), os_, _ptr(ws),
-                           ws.numel(), _stream()), "tq_lora")
+        ws = _workspace_ptr(ws, 0 if ws is not None else tq_lora_workspace(lora, m), dev)
+        st = _lib().tq_lora(lora._ref, x.data_ptr(), m, adapter.data_ptr(), y.data_ptr(), lora.n if m <= 1 else y.stride(0),
+                            out.data_ptr(), lora.n if m <= 1 else out.stride(0), ws.data_ptr(), ws.numel(),
+                            torch.cuda.current_stream().cuda_stream)
+    _ok(st, "tq_lora")
     return out

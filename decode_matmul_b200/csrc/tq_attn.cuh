@@ -53,8 +53,7 @@ struct AttnCfg {
   static constexpr int EB = KvElem<T>::bytes;
   static constexpr int RB = D * EB;          // bytes of a key
   static constexpr int CPR = RB / 16;        // 16-byte chunks of a key
-  static constexpr int STRIDE = RB + 16;     // shared-memory row: an odd number of chunks (no bank conflicts)
-  static constexpr int STAGE = 2 * 16 * STRIDE;
+  static constexpr int STAGE = 2 * 16 * RB;  // 16 keys and 16 values
   static constexpr int COLS = 8 * NT;        // head columns
   static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
   static constexpr int SLOT = PART * 4;
@@ -67,6 +66,14 @@ struct AttnCfg {
   static constexpr int WARP_BYTES = RING + SLOT;
   static constexpr int SMEM = WARPS * WARP_BYTES + CTL;
   static constexpr int THREADS = WARPS * 32;
+  // Chunk ch of key row r lies at chunk ch ^ swz(r) of its row, so that the
+  // same chunk of 8 rows in a row (one ldmatrix phase) is in 8 different
+  // 16-byte banks; the xor stays inside aligned groups, so rows of any of
+  // these sizes map onto themselves.
+  static __host__ __device__ constexpr int swz(int r) {
+    return CPR % 8 == 0 ? (r & 7) : (CPR % 4 == 0 ? ((r >> 1) & 3) : ((r >> 2) & 1));
+  }
+  static_assert(CPR % 8 == 0 || CPR == 4 || CPR == 12 || CPR == 6, "row sizes the swizzle covers");
   static_assert(STAGES >= 2 && SMEM <= 227 * 1024 && WARP_BYTES % 16 == 0, "ring");
 };
 
@@ -117,28 +124,35 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
     mma_16816(c, a, b0, b1);
 }
 
-// Where a warp stands in the tile order.
-struct AttnWalk {
-  int64_t row_tile;  // first tile of the row (of the whole call's order)
-  int32_t row, item, j;  // row, item in the row, tile in the item
-  int32_t n;      // tiles of an item of this row (at least one, so that rows without keys are written too)
-  int32_t keys, first, seq;  // visible keys, the first of them, block-table row
+// The visible keys of a row.
+struct AttnRow {
+  int32_t keys, first, seq;  // how many, the first of them, block-table row
+  // tiles of an item of the row: at least one, so that rows without keys are written too
+  __device__ __forceinline__ int32_t tiles() const { return keys > 0 ? (int32_t)(((uint32_t)keys + 15u) >> 4) : 1; }
 };
 
-__device__ __forceinline__ int32_t attn_keys(const AttnParams& p, int row, int32_t& first, int32_t& seq, bool& bad) {
+// Where a warp stands in the tile order.
+struct AttnWalk {
+  int64_t row_tile;      // first tile of the row (of the whole call's order)
+  int32_t row, item, j;  // row, item in the row, tile in the item
+  int32_t n;             // tiles of an item of this row
+  AttnRow r;
+};
+
+// bad: the row's sequence or position is outside the block table
+__device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int row, bool& bad) {
+  AttnRow r;
   const int32_t pos = p.pos[row];
-  seq = p.seq ? p.seq[row] : row;
-  bad = pos >= 0 && (seq < 0 || seq >= p.c.n_seqs || pos >= p.c.page_size * p.c.max_pages);
-  first = 0;
-  if (pos < 0 || bad) return 0;
-  if (p.window > 0 && pos >= p.window) first = pos - p.window + 1;
-  return pos - first + 1;
+  r.seq = p.seq ? p.seq[row] : row;
+  bad = pos >= 0 && (r.seq < 0 || r.seq >= p.c.n_seqs || pos >= p.c.page_size * p.c.max_pages);
+  r.first = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+  r.keys = pos < 0 || bad ? 0 : pos - r.first + 1;
+  return r;
 }
 
-__device__ __forceinline__ void attn_row(const AttnParams& p, AttnWalk& w) {
-  bool bad;
-  w.keys = attn_keys(p, w.row, w.first, w.seq, bad);
-  w.n = w.keys > 0 ? (int32_t)(((uint32_t)w.keys + 15u) >> 4) : 1;
+// a / b, without the long division where the values allow it
+__device__ __forceinline__ int64_t quot(int64_t a, int32_t b) {
+  return ((uint64_t)a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 __device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int items) {
@@ -147,7 +161,11 @@ __device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int 
   if (++w.item < items) return;
   w.item = 0;
   w.row_tile += (int64_t)w.n * items;
-  if (++w.row < p.m) attn_row(p, w);
+  if (++w.row < p.m) {
+    bool bad;
+    w.r = attn_row(p, w.row, bad);
+    w.n = w.r.tiles();
+  }
 }
 
 template <int T, int D, int NT>
@@ -164,9 +182,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   };
   struct Ctl {
     int64_t warp_sum[W];
-    int64_t row_tile[W];
-    int32_t row[W];
-    Seg seg[W][2];
+    AttnWalk at[W];  // where each warp's range begins
+    Seg seg[2 * W];  // what warp w left in its head (2w) and tail (2w+1) slot
     int32_t last;
   };
   static_assert(sizeof(Ctl) <= C::CTL, "control block");
@@ -178,60 +195,111 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   pdl_launch_dependents();
 
   // ---- the split: prefix sums of the rows' tiles -------------------------------
-  const int per = (p.m + C::THREADS - 1) / C::THREADS;
-  const int r0 = tid * per < p.m ? tid * per : p.m;
-  const int r1 = r0 + per < p.m ? r0 + per : p.m;
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    AttnWalk w;
-    bool bad;
-    const int32_t keys = attn_keys(p, r, w.first, w.seq, bad);
-    if (bad && blockIdx.x == 0) flag_bad_index(p.status);
-    mine += keys > 0 ? (((uint32_t)keys + 15u) >> 4) : 1;
-  }
-  int64_t incl = mine;
+  // Up to 32 rows every warp sums them for itself (a row per lane, no barrier);
+  // more are shared among the block's threads.
+  AttnWalk cw;        // where this warp stands
+  int64_t left;       // tiles of this warp
+  int64_t b0, total, share;  // block c takes share tiles, one more when c < rest
+  int32_t blocks, rest;
+  auto split = [&](int64_t rows_total) {
+    total = rows_total * items;
+    blocks = gridDim.x;
+    if (total < (int64_t)blocks * p.min_tiles) blocks = ((int32_t)total + p.min_tiles - 1) / p.min_tiles;
+    share = quot(total, blocks);
+    rest = (int32_t)(total - share * blocks);
+    const int32_t c = blockIdx.x;
+    b0 = c * share + (c < rest ? c : rest);
+  };
+  // first tile of warp w (of the block's share: an even split again)
+  auto warp_first = [&](int w) {
+    const int64_t len = share + ((int32_t)blockIdx.x < rest ? 1 : 0);
+    const int64_t ls = quot(len, W);
+    const int32_t lr = (int32_t)(len - ls * W);
+    return b0 + w * ls + (w < lr ? w : lr);
+  };
+  auto place = [](AttnWalk& w, int64_t o) {  // tile o of the row
+    w.item = (int32_t)quot(o, w.n);
+    w.j = (int32_t)(o - (int64_t)w.item * w.n);
+  };
+  if (tid < 2 * W) ctl->seg[tid].n = 0;
+  if (p.m <= 32) {
+    AttnRow r = {0, 0, 0};
+    bool bad = false;
+    if (lane < p.m) r = attn_row(p, lane, bad);
+    if (bad && blockIdx.x == 0 && warp == 0) flag_bad_index(p.status);
+    const int32_t n = lane < p.m ? r.tiles() : 0;
+    int64_t incl = n;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += v;
-  }
-  if (lane == 31) ctl->warp_sum[warp] = incl;
-  if (tid < W * 2) ctl->seg[tid >> 1][tid & 1].n = 0;
-  __syncthreads();
-  int64_t before = 0, rows_total = 0;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    split(__shfl_sync(0xffffffffu, incl, 31));
+    if ((int32_t)blockIdx.x >= blocks) return;
+    const int64_t w0 = warp_first(warp);
+    left = warp_first(warp + 1) - w0;
+    const int64_t at = (incl - n) * items;
+    const int src = __ffs(__ballot_sync(0xffffffffu, w0 >= at && w0 < incl * items)) - 1;  // none when left is 0 at the end
+    const int sl = src < 0 ? 0 : src;
+    cw.row = sl;
+    cw.row_tile = __shfl_sync(0xffffffffu, at, sl);
+    cw.n = __shfl_sync(0xffffffffu, n, sl);
+    cw.r.keys = __shfl_sync(0xffffffffu, r.keys, sl);
+    cw.r.first = __shfl_sync(0xffffffffu, r.first, sl);
+    cw.r.seq = __shfl_sync(0xffffffffu, r.seq, sl);
+    place(cw, w0 - cw.row_tile);
+    __syncthreads();
+  } else {
+    const int per = (p.m + C::THREADS - 1) / C::THREADS;
+    const int r0 = tid * per < p.m ? tid * per : p.m;
+    const int r1 = r0 + per < p.m ? r0 + per : p.m;
+    int64_t mine = 0;
+    for (int i = r0; i < r1; ++i) {
+      bool bad;
+      mine += attn_row(p, i, bad).tiles();
+      if (bad && blockIdx.x == 0) flag_bad_index(p.status);
+    }
+    int64_t incl = mine;
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (i < warp) before += ctl->warp_sum[i];
-    rows_total += ctl->warp_sum[i];
-  }
-  const int64_t total = rows_total * items;
-  int64_t blocks = (total + p.min_tiles - 1) / p.min_tiles;
-  if (blocks > gridDim.x) blocks = gridDim.x;
-  if (blockIdx.x >= blocks) return;
-  const int64_t b0 = total * blockIdx.x / blocks, b1 = total * (blockIdx.x + 1) / blocks;
-  {
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) ctl->warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, rows_total = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i < warp) before += ctl->warp_sum[i];
+      rows_total += ctl->warp_sum[i];
+    }
+    split(rows_total);
+    if ((int32_t)blockIdx.x >= blocks) return;
+    const int64_t b1 = warp_first(W);
     int64_t at = (before + incl - mine) * items;  // first tile of row r0
-    const int64_t end = (before + incl) * items;
-    if (end > b0 && at < b1) {
-      for (int r = r0; r < r1; ++r) {
+    if ((before + incl) * items > b0 && at < b1) {
+      for (int i = r0; i < r1; ++i) {
         AttnWalk w;
-        w.row = r;
-        attn_row(p, w);
-        const int64_t nx = at + (int64_t)w.n * items;
-        for (int i = 0; i < W; ++i) {
-          const int64_t s = b0 + (b1 - b0) * i / W;
-          if (s >= at && s < nx) {
-            ctl->row[i] = r;
-            ctl->row_tile[i] = at;
+        bool bad;
+        w.r = attn_row(p, i, bad);
+        w.n = w.r.tiles();
+        w.row = i;
+        w.row_tile = at;
+        at += (int64_t)w.n * items;
+        for (int k = 0; k < W; ++k) {
+          const int64_t s = warp_first(k);
+          if (s >= w.row_tile && s < at) {
+            place(w, s - w.row_tile);
+            ctl->at[k] = w;
           }
         }
-        at = nx;
       }
     }
+    __syncthreads();
+    const int64_t w0 = warp_first(warp);
+    left = warp_first(warp + 1) - w0;
+    cw = ctl->at[warp];
   }
-  __syncthreads();
-  const int64_t w0 = b0 + (b1 - b0) * warp / W, w1 = b0 + (b1 - b0) * (warp + 1) / W;
-  int64_t left = w1 - w0;  // tiles of this warp
 
   uint8_t* ring = smem + warp * C::WARP_BYTES;
   float* head_slot = reinterpret_cast<float*>(ring + C::RING);  // O of the first item when it began before the warp
@@ -239,15 +307,6 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   const uint32_t ring_u = smem_u32(ring);
 
   if (left > 0) {
-    AttnWalk cw;  // consumer
-    cw.row = ctl->row[warp];
-    cw.row_tile = ctl->row_tile[warp];
-    attn_row(p, cw);
-    {
-      const int64_t o = w0 - cw.row_tile;
-      cw.item = (int32_t)(o / cw.n);
-      cw.j = (int32_t)(o - (int64_t)cw.item * cw.n);
-    }
     AttnWalk pw = cw;  // producer: the tile whose pages are looked up next
     int64_t to_look = left;
 
@@ -259,10 +318,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       valid = false;
       if (to_look > 0) {
         const int32_t idx = (pw.j << 4) + (lane & 15);
-        if (idx < pw.keys) {
-          const uint32_t t = (uint32_t)(pw.first + idx);
+        if (idx < pw.r.keys) {
+          const uint32_t t = (uint32_t)(pw.r.first + idx);
           const uint32_t pi = (__umulhi(t, p.page_mul) + t) >> p.page_shift;
-          page = p.c.pages[(int64_t)pw.seq * p.c.max_pages + pi];
+          page = p.c.pages[(int64_t)pw.r.seq * p.c.max_pages + pi];
           off = (int64_t)(t - pi * (uint32_t)p.c.page_size) * p.c.token_stride +
                 (int64_t)(pw.item / p.head_groups) * p.c.head_stride;
           valid = true;
@@ -290,9 +349,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
           const int r = c / C::CPR, ch = c - r * C::CPR;
           const int64_t ro = __shfl_sync(0xffffffffu, o, r);
           const int64_t bo = (ro < 0 ? 0 : ro) * C::EB + ch * 16;
-          const uint32_t d = base + r * C::STRIDE + ch * 16;
+          const uint32_t d = base + r * C::RB + (ch ^ C::swz(r)) * 16;
           cp_async16(d, static_cast<const uint8_t*>(p.c.k) + (ro < 0 ? 0 : bo), ro >= 0);
-          cp_async16(d + 16 * C::STRIDE, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
+          cp_async16(d + 16 * C::RB, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
         }
       }
       cp_async_commit();
@@ -364,19 +423,22 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 
       if (vm) {
         const uint32_t kb = ring_u + stage_out * C::STAGE;
-        const uint32_t vb = kb + 16 * C::STRIDE;
+        const uint32_t vb = kb + 16 * C::RB;
         // S^T
         float s[NT][4], s2[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
-        const uint32_t ka = kb + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::STRIDE + (lane >> 4) * 16;
+        // this lane's row of the 8x8 matrices, and its chunk: ((step, half) ^ swz(row)) * 16
+        const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t ka = kb + krow * C::RB;
+        const uint32_t kx = ((lane >> 4) ^ C::swz(krow)) * 16;
         if constexpr (!F8) {
 #pragma unroll
           for (int ks = 0; ks < MT; ++ks) {
             uint32_t a[4];
-            ldsm4(a, ka + ks * 32);
+            ldsm4(a, ka + (kx ^ (ks * 32)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16<BF>((ks & 1) ? s2[nt] : s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
           }
@@ -384,7 +446,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 #pragma unroll
           for (int ks = 0; ks < MT; ks += 2) {
             uint32_t r[4];
-            ldsm4(r, ka + ks * 16);
+            ldsm4(r, ka + (kx ^ (ks * 16)));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t a[4] = {e4m3x2_to_h2(r[2 * u]), e4m3x2_to_h2(r[2 * u + 1]), e4m3x2_to_h2(r[2 * u] >> 16),
@@ -460,11 +522,13 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         }
         // O^T
         if constexpr (!F8) {
-          const uint32_t va = vb + ((lane & 7) + (lane >> 4) * 8) * C::STRIDE + ((lane >> 3) & 1) * 16;
+          const int vrow = (lane & 7) + (lane >> 4) * 8;
+          const uint32_t va = vb + vrow * C::RB;
+          const uint32_t vx = (((lane >> 3) & 1) ^ C::swz(vrow)) * 16;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             uint32_t a[4];
-            ldsm4_t(a, va + mt * 32);
+            ldsm4_t(a, va + (vx ^ (mt * 32)));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma16<BF>(o[mt][nt], a, ph[nt][0], ph[nt][1]);
@@ -474,11 +538,11 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         } else {
           // a 16-bit element of the transposed load is a pair of neighbouring
           // features: MMA rows r and r + 8 are features 2r and 2r + 1
-          const uint32_t va = vb + ((lane & 7) + ((lane >> 3) & 1) * 8) * C::STRIDE + (lane >> 4) * 16;
+          const uint32_t va = vb + krow * C::RB;
 #pragma unroll
           for (int mt = 0; mt < MT; mt += 2) {
             uint32_t r[4];
-            ldsm4_t(r, va + mt * 16);
+            ldsm4_t(r, va + (kx ^ (mt * 16)));
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t x = __byte_perm(r[2 * u], 0, 0x3120), y = __byte_perm(r[2 * u + 1], 0, 0x3120);
@@ -556,7 +620,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               }
           }
           if (lane == 0) {
-            Seg& g = ctl->seg[warp][slot];
+            Seg& g = ctl->seg[2 * warp + slot];
             g.start = cw.row_tile + (int64_t)cw.item * cw.n;
             g.n = cw.n;
             g.row = cw.row;
@@ -573,56 +637,88 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   __syncthreads();
 
   // ---- join: first the block's warps, then the blocks of an item ----------------
-  auto slot_ptr = [&](int i) {  // i = 2 warp + slot
-    uint8_t* b = smem + (i >> 1) * C::WARP_BYTES;
-    return reinterpret_cast<const float*>((i & 1) ? b : b + C::RING);
+  // parts: O, M, L relative to their own maxima; joined sum_i 2^(M_i - M) O_i
+  auto block_of = [&](int64_t tile) {
+    const int64_t lead = (int64_t)rest * (share + 1);
+    return tile < lead ? (int32_t)quot(tile, (int32_t)(share + 1)) : rest + (int32_t)quot(tile - lead, (int32_t)share);
   };
-  auto block_of = [&](int64_t tile) { return (int)(((tile + 1) * blocks - 1) / total); };
   constexpr int QUADS = D * COLS / 4;  // float4 of an O
   constexpr int QPT = (QUADS + C::THREADS - 1) / C::THREADS;
-  for (int i = 0; i < 2 * W;) {
-    const Seg g = ctl->seg[i >> 1][i & 1];
-    if (g.n == 0) {
-      ++i;
-      continue;
-    }
-    int e = i + 1;  // segments [i, e) are of this item
-    while (e < 2 * W) {
-      const Seg& x = ctl->seg[e >> 1][e & 1];
-      if (x.n != 0 && x.start != g.start) break;
-      ++e;
-    }
+  constexpr bool FULL = QUADS % C::THREADS == 0;
+  constexpr int BATCH = QPT <= 2 ? 4 : 2;  // blocks' parts in flight together
+  const int col = (tid * 4) % COLS;  // the same for all of a thread's quads
+  static_assert((C::THREADS * 4) % COLS == 0, "columns");
+  float4 acc[QPT];
+  float M[4], L[4];
+  int64_t my_start = -1 - lane;
+  uint32_t live;
+  {
+    const bool on = lane < 2 * W && ctl->seg[lane].n != 0;
+    if (on) my_start = ctl->seg[lane].start;
+    live = __ballot_sync(0xffffffffu, on);
+  }
+  const uint32_t same = __match_any_sync(0xffffffffu, (unsigned long long)my_start);
+  while (live) {  // the same in every warp
+    const int first = __ffs(live) - 1;
+    const uint32_t parts = __shfl_sync(0xffffffffu, same, first);
+    live &= ~parts;
+    const Seg g = ctl->seg[first];
     const int c_first = block_of(g.start), c_last = block_of(g.start + g.n - 1);
-    const bool whole = c_first == c_last;
-    float* gp = p.partials + ((int64_t)blockIdx.x * 2 + (c_first == (int)blockIdx.x ? 1 : 0)) * C::PART;
-    float4 acc[QPT];
-    float M[4], L[4];
-    const int col = (tid * 4) % COLS;  // the same for all of a thread's quads (THREADS * 4 is a multiple of COLS)
-    // weights of each part from its M: sum_i 2^(M_i - M) O_i, and so for L
-    auto maxima = [&](const float* part) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) M[k] = fmaxf(M[k], part[D * COLS + col + k]);
+    for (int k = 0; k < 4; ++k) {
+      M[k] = -INFINITY;
+      L[k] = 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto slot = [&](int k) {
+      const uint8_t* b = smem + (k >> 1) * C::WARP_BYTES;
+      return reinterpret_cast<const float*>((k & 1) ? b : b + C::RING);
     };
-    auto add = [&](const float* part) {
-      float f[4];
+    auto weight = [&](float m, float top) { return top == -INFINITY ? 0.f : ex2(m - top); };
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[k] = M[k] == -INFINITY ? 0.f : ex2(part[D * COLS + col + k] - M[k]);
-        L[k] += f[k] * part[D * COLS + COLS + col + k];
+    for (int k = 0; k < 2 * W; ++k)
+      if (parts >> k & 1) {
+        const float4 m = *reinterpret_cast<const float4*>(slot(k) + D * COLS + col);
+        M[0] = fmaxf(M[0], m.x), M[1] = fmaxf(M[1], m.y), M[2] = fmaxf(M[2], m.z), M[3] = fmaxf(M[3], m.w);
       }
+#pragma unroll
+    for (int k = 0; k < 2 * W; ++k)
+      if (parts >> k & 1) {
+        const float* part = slot(k);
+        const float4 m = *reinterpret_cast<const float4*>(part + D * COLS + col);
+        const float4 l = *reinterpret_cast<const float4*>(part + D * COLS + COLS + col);
+        const float f[4] = {weight(m.x, M[0]), weight(m.y, M[1]), weight(m.z, M[2]), weight(m.w, M[3])};
+        L[0] += f[0] * l.x, L[1] += f[1] * l.y, L[2] += f[2] * l.z, L[3] += f[3] * l.w;
+#pragma unroll
+        for (int u = 0; u < QPT; ++u) {
+          const int qd = u * C::THREADS + tid;
+          if (FULL || qd < QUADS) {
+            const float4 v = *reinterpret_cast<const float4*>(part + qd * 4);
+            acc[u].x += f[0] * v.x, acc[u].y += f[1] * v.y, acc[u].z += f[2] * v.z, acc[u].w += f[3] * v.w;
+          }
+        }
+      }
+    if (c_first != c_last) {
+      // publish the block's part; the last block of the item to arrive joins all of them, in block order
+      float* gp = p.partials + ((int64_t)blockIdx.x * 2 + (c_first == (int)blockIdx.x)) * C::PART;
 #pragma unroll
       for (int u = 0; u < QPT; ++u) {
         const int qd = u * C::THREADS + tid;
-        if (QUADS % C::THREADS == 0 || qd < QUADS) {
-          const float4 v = *reinterpret_cast<const float4*>(part + qd * 4);
-          acc[u].x += f[0] * v.x;
-          acc[u].y += f[1] * v.y;
-          acc[u].z += f[2] * v.z;
-          acc[u].w += f[3] * v.w;
-        }
+        if (FULL || qd < QUADS) *reinterpret_cast<float4*>(gp + qd * 4) = acc[u];
       }
-    };
-    auto clear = [&]() {
+      if (tid < COLS / 4) {
+        *reinterpret_cast<float4*>(gp + D * COLS + col) = make_float4(M[0], M[1], M[2], M[3]);
+        *reinterpret_cast<float4*>(gp + D * COLS + COLS + col) = make_float4(L[0], L[1], L[2], L[3]);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) ctl->last = atomicAdd(p.counters + c_first, 1) == c_last - c_first;
+      __syncthreads();
+      const bool last = ctl->last != 0;
+      __syncthreads();  // read by all before the next item's write
+      if (!last) continue;
+      __threadfence();
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         M[k] = -INFINITY;
@@ -630,66 +726,69 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       }
 #pragma unroll
       for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    auto write = [&]() {
-      const int kvh = g.item / p.head_groups, hg = g.item - kvh * p.head_groups;
-      const float vsc = p.c.vs ? p.c.vs[kvh] : 1.f;
+      for (int c = c_first; c <= c_last; c += BATCH) {
+        float4 m[BATCH], l[BATCH], v[BATCH][QPT];
 #pragma unroll
-      for (int u = 0; u < QPT; ++u) {
-        const int qd = u * C::THREADS + tid;
-        if (QUADS % C::THREADS != 0 && qd >= QUADS) continue;
-        const int d = qd * 4 / COLS;
-        const float v[4] = {acc[u].x, acc[u].y, acc[u].z, acc[u].w};
+        for (int i = 0; i < BATCH; ++i) {
+          // past the end: a part of weight zero
+          m[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          l[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < QPT; ++u) v[i][u] = l[i];
+          if (c + i <= c_last) {
+            const float* part = p.partials + ((int64_t)(c + i) * 2 + (c + i == c_first)) * C::PART;
+            m[i] = __ldcg(reinterpret_cast<const float4*>(part + D * COLS + col));
+            l[i] = __ldcg(reinterpret_cast<const float4*>(part + D * COLS + COLS + col));
+#pragma unroll
+            for (int u = 0; u < QPT; ++u) {
+              const int qd = u * C::THREADS + tid;
+              if (FULL || qd < QUADS) v[i][u] = __ldcg(reinterpret_cast<const float4*>(part + qd * 4));
+            }
+          }
+        }
+        float old[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) old[k] = M[k];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+          M[0] = fmaxf(M[0], m[i].x), M[1] = fmaxf(M[1], m[i].y), M[2] = fmaxf(M[2], m[i].z), M[3] = fmaxf(M[3], m[i].w);
+        float r[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int gh = hg * COLS + col + k;
-          if (gh >= p.group) continue;
-          const float y = L[k] == 0.f ? 0.f : v[k] * (vsc / L[k]);
-          const int64_t at = ((int64_t)g.row * p.q_heads + kvh * p.group + gh) * D + d;
-          if (p.out_bf16)
-            static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(y);
-          else
-            static_cast<__half*>(p.out)[at] = __float2half_rn(y);
+          r[k] = weight(old[k], M[k]);
+          L[k] *= r[k];
+        }
+#pragma unroll
+        for (int u = 0; u < QPT; ++u) acc[u].x *= r[0], acc[u].y *= r[1], acc[u].z *= r[2], acc[u].w *= r[3];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const float f[4] = {weight(m[i].x, M[0]), weight(m[i].y, M[1]), weight(m[i].z, M[2]), weight(m[i].w, M[3])};
+          L[0] += f[0] * l[i].x, L[1] += f[1] * l[i].y, L[2] += f[2] * l[i].z, L[3] += f[3] * l[i].w;
+#pragma unroll
+          for (int u = 0; u < QPT; ++u)
+            acc[u].x += f[0] * v[i][u].x, acc[u].y += f[1] * v[i][u].y, acc[u].z += f[2] * v[i][u].z,
+                acc[u].w += f[3] * v[i][u].w;
         }
       }
-    };
-    clear();
-    for (int k = i; k < e; ++k)
-      if (ctl->seg[k >> 1][k & 1].n) maxima(slot_ptr(k));
-    for (int k = i; k < e; ++k)
-      if (ctl->seg[k >> 1][k & 1].n) add(slot_ptr(k));
-    if (whole) {
-      write();
-    } else {
-#pragma unroll
-      for (int u = 0; u < QPT; ++u) {
-        const int qd = u * C::THREADS + tid;
-        if (QUADS % C::THREADS == 0 || qd < QUADS) *reinterpret_cast<float4*>(gp + qd * 4) = acc[u];
-      }
-      if (tid < COLS / 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          gp[D * COLS + col + k] = M[k];
-          gp[D * COLS + COLS + col + k] = L[k];
-        }
-      }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) ctl->last = atomicAdd(p.counters + c_first, 1) == c_last - c_first;
-      __syncthreads();
-      if (ctl->last) {
-        __threadfence();
-        clear();
-        const float* pp = p.partials;
-        for (int c = c_first; c <= c_last; ++c) maxima(pp + ((int64_t)c * 2 + (c == c_first)) * C::PART);
-#pragma unroll 4
-        for (int c = c_first; c <= c_last; ++c) add(pp + ((int64_t)c * 2 + (c == c_first)) * C::PART);
-        write();
-        if (tid == 0) p.counters[c_first] = 0;
-      }
-      __syncthreads();
+      if (tid == 0) p.counters[c_first] = 0;
     }
-    i = e;
+    const int kvh = g.item / p.head_groups, g0 = (g.item - kvh * p.head_groups) * COLS + col;
+    const float vsc = p.c.vs ? p.c.vs[kvh] : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (g0 + k >= p.group) continue;
+      const float inv = L[k] == 0.f ? 0.f : vsc / L[k];
+      const int64_t at = ((int64_t)g.row * p.q_heads + kvh * p.group + g0 + k) * D;
+#pragma unroll
+      for (int u = 0; u < QPT; ++u) {
+        const int qd = u * C::THREADS + tid;
+        if (!FULL && qd >= QUADS) continue;
+        const float y = (k == 0 ? acc[u].x : k == 1 ? acc[u].y : k == 2 ? acc[u].z : acc[u].w) * inv;
+        const int d = qd * 4 / COLS;
+        static_cast<uint16_t*>(p.out)[at + d] =
+            p.out_bf16 ? f_to_bf16_bits(y) : __half_as_ushort(__float2half_rn(y));
+      }
+    }
   }
 }
 
