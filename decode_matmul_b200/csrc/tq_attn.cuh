@@ -39,7 +39,7 @@ struct AttnParams {
   int32_t m, q_heads, window;
   int32_t group;        // query heads per key head
   int32_t head_groups;  // items per key head
-  int32_t min_tiles;    // tiles a block takes at least before another is used
+  int32_t min_units;    // units a block takes at least before another is used
   uint32_t page_mul, page_shift;  // j / page_size = (umulhi(j, mul) + j) >> shift
   float scale;
   int32_t out_bf16;
@@ -53,15 +53,19 @@ struct AttnCfg {
   static constexpr int EB = KvElem<T>::bytes;
   static constexpr int RB = D * EB;          // bytes of a key
   static constexpr int CPR = RB / 16;        // 16-byte chunks of a key
-  static constexpr int STAGE = 2 * 16 * RB;  // 16 keys and 16 values
+  // keys of a tile: 32 where 64 KB of ring per 8 warps then still hold it
+  // (longer independent chains per step), else 16
+  static constexpr int TK = RB <= 128 ? 32 : 16;
+  static constexpr int KT = TK / 16;
+  static constexpr int STAGE = 2 * TK * RB;  // the keys, then the values
   static constexpr int COLS = 8 * NT;        // head columns
   static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
   static constexpr int SLOT = PART * 4;
-  static constexpr int CTL = 2048;
+  static constexpr int CTL = 3072;
   static constexpr int fit(int warps) { return ((227 * 1024 - CTL) / warps - SLOT) / STAGE; }
   // as many warps as leave each a ring of three tiles, else four
   static constexpr int WARPS = fit(8) >= 3 ? 8 : (fit(6) >= 3 ? 6 : 4);
-  static constexpr int STAGES = fit(WARPS) > 4 ? 4 : fit(WARPS);
+  static constexpr int STAGES = fit(WARPS) > 3 ? 3 : fit(WARPS);
   static constexpr int RING = STAGES * STAGE > SLOT ? STAGES * STAGE : SLOT;  // the tail's partial reuses the ring
   static constexpr int WARP_BYTES = RING + SLOT;
   static constexpr int SMEM = WARPS * WARP_BYTES + CTL;
@@ -128,12 +132,21 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
 struct AttnRow {
   int32_t keys, first, seq;  // how many, the first of them, block-table row
   // tiles of an item of the row: at least one, so that rows without keys are written too
-  __device__ __forceinline__ int32_t tiles() const { return keys > 0 ? (int32_t)(((uint32_t)keys + 15u) >> 4) : 1; }
+  template <int TK>
+  __device__ __forceinline__ int32_t tiles() const {
+    return keys > 0 ? (int32_t)(((uint32_t)keys + TK - 1) / TK) : 1;
+  }
 };
+
+// An item of n tiles takes n + kItemCost units of the split: its start and end
+// (queries, partial or final output) cost about as much as two tiles, which
+// would leave the blocks that hold many short rows behind (64 rows of 3 to
+// 8192 keys: the slowest block took 1.35 times the mean without it).
+constexpr int kItemCost = 2;
 
 // Where a warp stands in the tile order.
 struct AttnWalk {
-  int64_t row_tile;      // first tile of the row (of the whole call's order)
+  int64_t row_at;        // first unit of the row in the whole call's order
   int32_t row, item, j;  // row, item in the row, tile in the item
   int32_t n;             // tiles of an item of this row
   AttnRow r;
@@ -155,16 +168,17 @@ __device__ __forceinline__ int64_t quot(int64_t a, int32_t b) {
   return ((uint64_t)a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+template <int TK>
 __device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int items) {
   if (++w.j < w.n) return;
   w.j = 0;
   if (++w.item < items) return;
   w.item = 0;
-  w.row_tile += (int64_t)w.n * items;
+  w.row_at += (int64_t)(w.n + kItemCost) * items;
   if (++w.row < p.m) {
     bool bad;
     w.r = attn_row(p, w.row, bad);
-    w.n = w.r.tiles();
+    w.n = w.r.tiles<TK>();
   }
 }
 
@@ -173,10 +187,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   using C = AttnCfg<T, D, NT>;
   constexpr bool BF = T == KV_BF16;
   constexpr bool F8 = T == KV_E4M3;
-  constexpr int W = C::WARPS, S = C::STAGES, COLS = C::COLS, MT = D / 16;
+  constexpr int W = C::WARPS, S = C::STAGES, COLS = C::COLS, MT = D / 16, TK = C::TK, KT = C::KT;
   extern __shared__ __align__(16) uint8_t smem[];
   struct Seg {
-    int64_t start;  // first tile of the segment's item
+    int64_t start;  // unit of the first tile of the segment's item
     int32_t n, row, item;  // n: its tiles, 0 = no segment
     int32_t pad;
   };
@@ -184,6 +198,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     int64_t warp_sum[W];
     AttnWalk at[W];  // where each warp's range begins
     Seg seg[2 * W];  // what warp w left in its head (2w) and tail (2w+1) slot
+    float weight[2 * W][COLS];  // of the parts of an item
+    float top[2][COLS];         // M and L of the joined parts
     int32_t last;
   };
   static_assert(sizeof(Ctl) <= C::CTL, "control block");
@@ -194,41 +210,56 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the split: prefix sums of the rows' tiles -------------------------------
-  // Up to 32 rows every warp sums them for itself (a row per lane, no barrier);
-  // more are shared among the block's threads.
-  AttnWalk cw;        // where this warp stands
-  int64_t left;       // tiles of this warp
-  int64_t b0, total, share;  // block c takes share tiles, one more when c < rest
+  // ---- the split: prefix sums of the rows' units --------------------------------
+  // Up to 128 rows every warp sums them for itself (four rows per lane at most,
+  // no barrier); more are shared among the block's threads.
+  AttnWalk cw;  // where this warp stands
+  int64_t u0, u1;            // units of this warp
+  int64_t b0, total, share;  // block c takes share units, one more when c < rest
   int32_t blocks, rest;
   auto split = [&](int64_t rows_total) {
     total = rows_total * items;
     blocks = gridDim.x;
-    if (total < (int64_t)blocks * p.min_tiles) blocks = ((int32_t)total + p.min_tiles - 1) / p.min_tiles;
+    if (total < (int64_t)blocks * p.min_units) blocks = ((int32_t)total + p.min_units - 1) / p.min_units;
     share = quot(total, blocks);
     rest = (int32_t)(total - share * blocks);
     const int32_t c = blockIdx.x;
     b0 = c * share + (c < rest ? c : rest);
   };
-  // first tile of warp w (of the block's share: an even split again)
+  // first unit of warp w (of the block's share: an even split again)
   auto warp_first = [&](int w) {
     const int64_t len = share + ((int32_t)blockIdx.x < rest ? 1 : 0);
     const int64_t ls = quot(len, W);
     const int32_t lr = (int32_t)(len - ls * W);
     return b0 + w * ls + (w < lr ? w : lr);
   };
-  auto place = [](AttnWalk& w, int64_t o) {  // tile o of the row
-    w.item = (int32_t)quot(o, w.n);
-    w.j = (int32_t)(o - (int64_t)w.item * w.n);
+  // the first tile at or after unit o of the row (it may be in the next row)
+  auto place = [&](AttnWalk& w, int64_t o) {
+    const int32_t unit = w.n + kItemCost;
+    w.item = (int32_t)quot(o, unit);
+    w.j = (int32_t)(o - (int64_t)w.item * unit) - kItemCost;
+    if (w.j < 0) w.j = 0;
   };
   if (tid < 2 * W) ctl->seg[tid].n = 0;
-  if (p.m <= 32) {
-    AttnRow r = {0, 0, 0};
-    bool bad = false;
-    if (lane < p.m) r = attn_row(p, lane, bad);
-    if (bad && blockIdx.x == 0 && warp == 0) flag_bad_index(p.status);
-    const int32_t n = lane < p.m ? r.tiles() : 0;
-    int64_t incl = n;
+  if (p.m <= 128) {
+    const int per = (p.m + 31) >> 5;
+    AttnRow r[4];
+    int32_t n[4];
+    int64_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = lane * per + i;
+      n[i] = 0;
+      r[i] = {0, 0, 0};
+      if (i < per && row < p.m) {
+        bool bad;
+        r[i] = attn_row(p, row, bad);
+        if (bad && blockIdx.x == 0 && warp == 0) flag_bad_index(p.status);
+        n[i] = r[i].tiles<TK>();
+        mine += n[i] + kItemCost;
+      }
+    }
+    int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
@@ -236,18 +267,24 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     }
     split(__shfl_sync(0xffffffffu, incl, 31));
     if ((int32_t)blockIdx.x >= blocks) return;
-    const int64_t w0 = warp_first(warp);
-    left = warp_first(warp + 1) - w0;
-    const int64_t at = (incl - n) * items;
-    const int src = __ffs(__ballot_sync(0xffffffffu, w0 >= at && w0 < incl * items)) - 1;  // none when left is 0 at the end
+    u0 = warp_first(warp);
+    u1 = warp_first(warp + 1);
+    int64_t at = (incl - mine) * items;
+    const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= at && u0 < incl * items)) - 1;  // none when the range is empty
     const int sl = src < 0 ? 0 : src;
-    cw.row = sl;
-    cw.row_tile = __shfl_sync(0xffffffffu, at, sl);
-    cw.n = __shfl_sync(0xffffffffu, n, sl);
-    cw.r.keys = __shfl_sync(0xffffffffu, r.keys, sl);
-    cw.r.first = __shfl_sync(0xffffffffu, r.first, sl);
-    cw.r.seq = __shfl_sync(0xffffffffu, r.seq, sl);
-    place(cw, w0 - cw.row_tile);
+    AttnWalk w = {at, lane * per, 0, 0, n[0], r[0]};
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+      at += (int64_t)(n[i - 1] ? n[i - 1] + kItemCost : 0) * items;
+      if (n[i] && u0 >= at) w = {at, lane * per + i, 0, 0, n[i], r[i]};
+    }
+    cw.row = __shfl_sync(0xffffffffu, w.row, sl);
+    cw.row_at = __shfl_sync(0xffffffffu, w.row_at, sl);
+    cw.n = __shfl_sync(0xffffffffu, w.n, sl);
+    cw.r.keys = __shfl_sync(0xffffffffu, w.r.keys, sl);
+    cw.r.first = __shfl_sync(0xffffffffu, w.r.first, sl);
+    cw.r.seq = __shfl_sync(0xffffffffu, w.r.seq, sl);
+    place(cw, u0 - cw.row_at);
     __syncthreads();
   } else {
     const int per = (p.m + C::THREADS - 1) / C::THREADS;
@@ -256,7 +293,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     int64_t mine = 0;
     for (int i = r0; i < r1; ++i) {
       bool bad;
-      mine += attn_row(p, i, bad).tiles();
+      mine += attn_row(p, i, bad).tiles<TK>() + kItemCost;
       if (bad && blockIdx.x == 0) flag_bad_index(p.status);
     }
     int64_t incl = mine;
@@ -276,48 +313,50 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     split(rows_total);
     if ((int32_t)blockIdx.x >= blocks) return;
     const int64_t b1 = warp_first(W);
-    int64_t at = (before + incl - mine) * items;  // first tile of row r0
+    int64_t at = (before + incl - mine) * items;  // first unit of row r0
     if ((before + incl) * items > b0 && at < b1) {
       for (int i = r0; i < r1; ++i) {
         AttnWalk w;
         bool bad;
         w.r = attn_row(p, i, bad);
-        w.n = w.r.tiles();
+        w.n = w.r.tiles<TK>();
         w.row = i;
-        w.row_tile = at;
-        at += (int64_t)w.n * items;
+        w.row_at = at;
+        at += (int64_t)(w.n + kItemCost) * items;
         for (int k = 0; k < W; ++k) {
           const int64_t s = warp_first(k);
-          if (s >= w.row_tile && s < at) {
-            place(w, s - w.row_tile);
+          if (s >= w.row_at && s < at) {
+            place(w, s - w.row_at);
             ctl->at[k] = w;
           }
         }
       }
     }
     __syncthreads();
-    const int64_t w0 = warp_first(warp);
-    left = warp_first(warp + 1) - w0;
-    cw = ctl->at[warp];
+    u0 = warp_first(warp);
+    u1 = warp_first(warp + 1);
+    if (u0 < u1) cw = ctl->at[warp];
   }
+  // unit of the tile that a walk stands at
+  auto unit_of = [&](const AttnWalk& w) { return w.row_at + (int64_t)w.item * (w.n + kItemCost) + kItemCost + w.j; };
 
   uint8_t* ring = smem + warp * C::WARP_BYTES;
   float* head_slot = reinterpret_cast<float*>(ring + C::RING);  // O of the first item when it began before the warp
   float* tail_slot = reinterpret_cast<float*>(ring);            // O of the last item when it goes on (ring drained)
   const uint32_t ring_u = smem_u32(ring);
 
-  if (left > 0) {
+  if (u0 < u1 && unit_of(cw) < u1) {
     AttnWalk pw = cw;  // producer: the tile whose pages are looked up next
-    int64_t to_look = left;
+    bool more = true;  // pw stands at a tile of this warp
 
-    // look-up state of the producer: lane l < 16 holds key l of the tile
+    // look-up state of the producer: lane l < TK holds key l of the tile
     int32_t page = 0;
     int64_t off = 0;  // offset inside the page, head included
     bool valid = false;
     auto look = [&]() {
       valid = false;
-      if (to_look > 0) {
-        const int32_t idx = (pw.j << 4) + (lane & 15);
+      if (more) {
+        const int32_t idx = pw.j * TK + (lane & (TK - 1));
         if (idx < pw.r.keys) {
           const uint32_t t = (uint32_t)(pw.r.first + idx);
           const uint32_t pi = (__umulhi(t, p.page_mul) + t) >> p.page_shift;
@@ -326,11 +365,11 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
                 (int64_t)(pw.item / p.head_groups) * p.c.head_stride;
           valid = true;
         }
-        --to_look;
-        if (to_look > 0) attn_next(p, pw, items);
+        attn_next<TK>(p, pw, items);
+        more = pw.row < p.m && unit_of(pw) < u1;
       }
     };
-    uint64_t masks = 0;  // valid keys of the tiles in flight, 16 bits each, the oldest highest
+    uint64_t masks = 0;  // valid keys of the tiles in flight, TK bits each, the oldest highest
     int stage_in = 0;
     auto copy = [&]() {  // start the copies of the looked-up tile
       bool ok = valid;
@@ -339,19 +378,19 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         ok = false;
       }
       const int64_t o = ok ? (int64_t)page * p.c.page_stride + off : -1;
-      const uint32_t vm = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-      masks = (masks << 16) | vm;
+      const uint32_t vm = __ballot_sync(0xffffffffu, ok) & (0xffffffffu >> (32 - TK));
+      masks = (masks << TK) | vm;
       if (vm) {
         const uint32_t base = ring_u + stage_in * C::STAGE;
 #pragma unroll
-        for (int i = 0; i < C::CPR / 2; ++i) {
+        for (int i = 0; i < C::CPR * TK / 32; ++i) {
           const int c = i * 32 + lane;
           const int r = c / C::CPR, ch = c - r * C::CPR;
           const int64_t ro = __shfl_sync(0xffffffffu, o, r);
           const int64_t bo = (ro < 0 ? 0 : ro) * C::EB + ch * 16;
           const uint32_t d = base + r * C::RB + (ch ^ C::swz(r)) * 16;
           cp_async16(d, static_cast<const uint8_t*>(p.c.k) + (ro < 0 ? 0 : bo), ro >= 0);
-          cp_async16(d + 16 * C::RB, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
+          cp_async16(d + TK * C::RB, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
         }
       }
       cp_async_commit();
@@ -380,7 +419,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       return g < p.group ? kvh * p.group + g : -1;
     };
 
-    for (; left > 0; --left) {
+    for (bool done = false; !done;) {
       if (fresh) {
         fresh = false;
         const int kvh = cw.item / p.head_groups;
@@ -417,55 +456,68 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 
       cp_async_wait<S - 2>();
       __syncwarp();
-      const uint32_t vm = (uint32_t)(masks >> (16 * (S - 2))) & 0xffffu;
+      const uint32_t vm = (uint32_t)(masks >> (TK * (S - 2))) & (0xffffffffu >> (32 - TK));
       copy();  // into the stage that the previous tile has left
       look();
 
       if (vm) {
         const uint32_t kb = ring_u + stage_out * C::STAGE;
-        const uint32_t vb = kb + 16 * C::RB;
-        // S^T
-        float s[NT][4], s2[NT][4];
+        const uint32_t vb = kb + TK * C::RB;
+        // S^T, in two independent sums per 16 keys
+        float s[KT][NT][4], s2[KT][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[kt][nt][i] = 0.f;
         // this lane's row of the 8x8 matrices, and its chunk: ((step, half) ^ swz(row)) * 16
         const int krow = (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t ka = kb + krow * C::RB;
         const uint32_t kx = ((lane >> 4) ^ C::swz(krow)) * 16;
         if constexpr (!F8) {
 #pragma unroll
-          for (int ks = 0; ks < MT; ++ks) {
-            uint32_t a[4];
-            ldsm4(a, ka + (kx ^ (ks * 32)));
+          for (int ks = 0; ks < MT; ++ks)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16<BF>((ks & 1) ? s2[nt] : s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-          }
+            for (int kt = 0; kt < KT; ++kt) {
+              uint32_t a[4];
+              ldsm4(a, ka + kt * 16 * C::RB + (kx ^ (ks * 32)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma16<BF>((ks & 1) ? s2[kt][nt] : s[kt][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+            }
         } else {
 #pragma unroll
-          for (int ks = 0; ks < MT; ks += 2) {
-            uint32_t r[4];
-            ldsm4(r, ka + (kx ^ (ks * 16)));
+          for (int ks = 0; ks < MT; ks += 2)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t a[4] = {e4m3x2_to_h2(r[2 * u]), e4m3x2_to_h2(r[2 * u + 1]), e4m3x2_to_h2(r[2 * u] >> 16),
-                                     e4m3x2_to_h2(r[2 * u + 1] >> 16)};
+            for (int kt = 0; kt < KT; ++kt) {
+              uint32_t r[4];
+              ldsm4(r, ka + kt * 16 * C::RB + (kx ^ (ks * 16)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16<BF>(u ? s2[nt] : s[nt], a, qf[nt][ks + u][0], qf[nt][ks + u][1]);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t a[4] = {e4m3x2_to_h2(r[2 * u]), e4m3x2_to_h2(r[2 * u + 1]), e4m3x2_to_h2(r[2 * u] >> 16),
+                                       e4m3x2_to_h2(r[2 * u + 1] >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16<BF>(u ? s2[kt][nt] : s[kt][nt], a, qf[nt][ks + u][0], qf[nt][ks + u][1]);
+              }
             }
-          }
         }
-        // softmax: lane holds keys lane/4 and lane/4 + 8 of heads 2(lane%4) and +1
-        const bool v0 = (vm >> (lane >> 2)) & 1, v1 = (vm >> ((lane >> 2) + 8)) & 1;
+        // softmax: lane holds keys lane/4 and lane/4 + 8 (of each 16) of heads 2(lane%4) and +1
         float tm[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            s[nt][i] = v0 ? (s[nt][i] + s2[nt][i]) * sc : -INFINITY;
-            s[nt][i + 2] = v1 ? (s[nt][i + 2] + s2[nt][i + 2]) * sc : -INFINITY;
-            tm[nt][i] = fmaxf(s[nt][i], s[nt][i + 2]);
+            tm[nt][i] = -INFINITY;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                float& x = s[kt][nt][2 * r + i];
+                x = (vm >> (kt * 16 + r * 8 + (lane >> 2))) & 1 ? (x + s2[kt][nt][2 * r + i]) * sc : -INFINITY;
+                tm[nt][i] = fmaxf(tm[nt][i], x);
+              }
           }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
@@ -498,27 +550,32 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         // fp16 caches; at most 1, exact for a key that takes all); bf16
         // caches need bf16 weights, whose 2^-9 would be felt in the output,
         // so they go in as two terms (2^-17) and two MMAs.
-        uint32_t ph[NT][2], pl[NT][2];
+        uint32_t ph[KT][NT][2], pl[KT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
+          float m0[2];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            float e[2];
+          for (int i = 0; i < 2; ++i) m0[i] = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float m0 = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
-              e[i] = ex2(s[nt][2 * r + i] - m0);
-              sum[nt][i] += e[i];
+          for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float e[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                e[i] = ex2(s[kt][nt][2 * r + i] - m0[i]);
+                sum[nt][i] += e[i];
+              }
+              if constexpr (BF) {
+                const uint32_t h = KvElem<KV_BF16>::pack2(e[0], e[1]);
+                const uint32_t l =
+                    KvElem<KV_BF16>::pack2(e[0] - __uint_as_float(h << 16), e[1] - __uint_as_float(h & 0xffff0000u));
+                ph[kt][nt][r] = transpose8(h);
+                pl[kt][nt][r] = transpose8(l);
+              } else {
+                ph[kt][nt][r] = transpose8(f2_to_h2(e[0], e[1]));
+              }
             }
-            if constexpr (BF) {
-              const uint32_t h = KvElem<KV_BF16>::pack2(e[0], e[1]);
-              const uint32_t l = KvElem<KV_BF16>::pack2(e[0] - __uint_as_float(h << 16), e[1] - __uint_as_float(h & 0xffff0000u));
-              ph[nt][r] = transpose8(h);
-              pl[nt][r] = transpose8(l);
-            } else {
-              ph[nt][r] = transpose8(f2_to_h2(e[0], e[1]));
-            }
-          }
         }
         // O^T
         if constexpr (!F8) {
@@ -526,39 +583,46 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
           const uint32_t va = vb + vrow * C::RB;
           const uint32_t vx = (((lane >> 3) & 1) ^ C::swz(vrow)) * 16;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            ldsm4_t(a, va + (vx ^ (mt * 32)));
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma16<BF>(o[mt][nt], a, ph[nt][0], ph[nt][1]);
-              if constexpr (BF) mma16<BF>(o[mt][nt], a, pl[nt][0], pl[nt][1]);
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              ldsm4_t(a, va + kt * 16 * C::RB + (vx ^ (mt * 32)));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma16<BF>(o[mt][nt], a, ph[kt][nt][0], ph[kt][nt][1]);
+                if constexpr (BF) mma16<BF>(o[mt][nt], a, pl[kt][nt][0], pl[kt][nt][1]);
+              }
             }
-          }
         } else {
           // a 16-bit element of the transposed load is a pair of neighbouring
           // features: MMA rows r and r + 8 are features 2r and 2r + 1
           const uint32_t va = vb + krow * C::RB;
 #pragma unroll
-          for (int mt = 0; mt < MT; mt += 2) {
-            uint32_t r[4];
-            ldsm4_t(r, va + (kx ^ (mt * 16)));
+          for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const uint32_t x = __byte_perm(r[2 * u], 0, 0x3120), y = __byte_perm(r[2 * u + 1], 0, 0x3120);
-              const uint32_t a[4] = {e4m3x2_to_h2(x), e4m3x2_to_h2(x >> 16), e4m3x2_to_h2(y), e4m3x2_to_h2(y >> 16)};
+            for (int mt = 0; mt < MT; mt += 2) {
+              uint32_t r[4];
+              ldsm4_t(r, va + kt * 16 * C::RB + (kx ^ (mt * 16)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, ph[nt][0], ph[nt][1]);
+              for (int u = 0; u < 2; ++u) {
+                const uint32_t x = __byte_perm(r[2 * u], 0, 0x3120), y = __byte_perm(r[2 * u + 1], 0, 0x3120);
+                const uint32_t a[4] = {e4m3x2_to_h2(x), e4m3x2_to_h2(x >> 16), e4m3x2_to_h2(y), e4m3x2_to_h2(y >> 16)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, ph[kt][nt][0], ph[kt][nt][1]);
+              }
             }
-          }
         }
       }
       if (++stage_out == S) stage_out = 0;
       __syncwarp();
 
       // ---- end of the item or of the warp's range ---------------------------------
+      const AttnWalk tile = cw;
       const bool item_end = cw.j + 1 == cw.n;
-      if (item_end || left == 1) {
+      attn_next<TK>(p, cw, items);
+      done = cw.row >= p.m || unit_of(cw) >= u1;
+      if (item_end || done) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
@@ -572,8 +636,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
             float inv[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) inv[i] = sum[nt][i] == 0.f ? 0.f : vscale / sum[nt][i];
-            const int h = head_of(cw.item, nt * 8 + (lane >> 2));
-            uint16_t* op = static_cast<uint16_t*>(p.out) + ((int64_t)cw.row * p.q_heads + (h < 0 ? 0 : h)) * D;
+            const int h = head_of(tile.item, nt * 8 + (lane >> 2));
+            uint16_t* op = static_cast<uint16_t*>(p.out) + ((int64_t)tile.row * p.q_heads + (h < 0 ? 0 : h)) * D;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               const float* v = o[mt][nt];
@@ -621,16 +685,15 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
           }
           if (lane == 0) {
             Seg& g = ctl->seg[2 * warp + slot];
-            g.start = cw.row_tile + (int64_t)cw.item * cw.n;
-            g.n = cw.n;
-            g.row = cw.row;
-            g.item = cw.item;
+            g.start = tile.row_at + (int64_t)tile.item * (tile.n + kItemCost) + kItemCost;
+            g.n = tile.n;
+            g.row = tile.row;
+            g.item = tile.item;
           }
         }
         began_before = false;
         fresh = true;
       }
-      attn_next(p, cw, items);
     }
     cp_async_wait<0>();
   }
@@ -664,41 +727,64 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     live &= ~parts;
     const Seg g = ctl->seg[first];
     const int c_first = block_of(g.start), c_last = block_of(g.start + g.n - 1);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      M[k] = -INFINITY;
-      L[k] = 0.f;
-    }
-#pragma unroll
-    for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto slot = [&](int k) {
       const uint8_t* b = smem + (k >> 1) * C::WARP_BYTES;
       return reinterpret_cast<const float*>((k & 1) ? b : b + C::RING);
     };
     auto weight = [&](float m, float top) { return top == -INFINITY ? 0.f : ex2(m - top); };
+    // the parts' weights: a lane per part, a half warp per column
+    for (int c = warp * 2 + (lane >> 4); c < COLS; c += 2 * W) {
+      const int k = lane & 15;
+      const bool in = k < 2 * W && (parts >> k & 1);
+      const float m = in ? slot(k)[D * COLS + c] : -INFINITY;
+      float l = in ? slot(k)[D * COLS + COLS + c] : 0.f, top = m;
 #pragma unroll
-    for (int k = 0; k < 2 * W; ++k)
-      if (parts >> k & 1) {
-        const float4 m = *reinterpret_cast<const float4*>(slot(k) + D * COLS + col);
-        M[0] = fmaxf(M[0], m.x), M[1] = fmaxf(M[1], m.y), M[2] = fmaxf(M[2], m.z), M[3] = fmaxf(M[3], m.w);
+      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      const float f = in ? weight(m, top) : 0.f;
+      l *= f;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      if (in) ctl->weight[k][c] = f;
+      if (k == 0) {
+        ctl->top[0][c] = top;
+        ctl->top[1][c] = l;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      M[k] = ctl->top[0][col + k];
+      L[k] = ctl->top[1][col + k];
+    }
+#pragma unroll
+    for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t rem = parts; rem;) {
+      // four parts at a time, the bits of rem in order
+      const float* part[4];
+      float4 f[4];
+      bool on[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        on[i] = rem != 0;
+        const int k = on[i] ? __ffs(rem) - 1 : first;
+        part[i] = slot(k);
+        f[i] = *reinterpret_cast<const float4*>(&ctl->weight[k][col]);
+        rem &= rem - 1;
       }
 #pragma unroll
-    for (int k = 0; k < 2 * W; ++k)
-      if (parts >> k & 1) {
-        const float* part = slot(k);
-        const float4 m = *reinterpret_cast<const float4*>(part + D * COLS + col);
-        const float4 l = *reinterpret_cast<const float4*>(part + D * COLS + COLS + col);
-        const float f[4] = {weight(m.x, M[0]), weight(m.y, M[1]), weight(m.z, M[2]), weight(m.w, M[3])};
-        L[0] += f[0] * l.x, L[1] += f[1] * l.y, L[2] += f[2] * l.z, L[3] += f[3] * l.w;
+      for (int u = 0; u < QPT; ++u) {
+        const int qd = u * C::THREADS + tid;
+        if (FULL || qd < QUADS) {
 #pragma unroll
-        for (int u = 0; u < QPT; ++u) {
-          const int qd = u * C::THREADS + tid;
-          if (FULL || qd < QUADS) {
-            const float4 v = *reinterpret_cast<const float4*>(part + qd * 4);
-            acc[u].x += f[0] * v.x, acc[u].y += f[1] * v.y, acc[u].z += f[2] * v.z, acc[u].w += f[3] * v.w;
+          for (int i = 0; i < 4; ++i) {
+            if (!on[i]) break;
+            const float4 v = *reinterpret_cast<const float4*>(part[i] + qd * 4);
+            acc[u].x += f[i].x * v.x, acc[u].y += f[i].y * v.y, acc[u].z += f[i].z * v.z, acc[u].w += f[i].w * v.w;
           }
         }
       }
+    }
+    __syncthreads();  // the weights are read before the next item's are written
     if (c_first != c_last) {
       // publish the block's part; the last block of the item to arrive joins all of them, in block order
       float* gp = p.partials + ((int64_t)blockIdx.x * 2 + (c_first == (int)blockIdx.x)) * C::PART;

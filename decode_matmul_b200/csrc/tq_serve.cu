@@ -71,7 +71,7 @@ int check_ws(const void* ws, size_t have, size_t need) {
 
 // Attention: one block per SM; two partial results per block.
 constexpr int kAttnMaxBlocks = 148;
-constexpr int kAttnMinTiles = 8;  // tiles of 16 keys a block takes before another is used
+constexpr int kAttnMinUnits = 12;  // tiles (and item costs) a block takes before another is used
 
 int attn_cols(const tq_kv_cache_t* c, int32_t q_heads) { return q_heads / c->kv_heads <= 8 ? 8 : 16; }
 
@@ -225,7 +225,7 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   p.group = q_heads / cache->kv_heads;
   const int cols = attn_cols(cache, q_heads);
   p.head_groups = (p.group + cols - 1) / cols;
-  p.min_tiles = kAttnMinTiles;
+  p.min_units = kAttnMinUnits;
   divider((uint32_t)cache->page_size, &p.page_mul, &p.page_shift);
   p.out_bf16 = out_dtype == TQ_BF16;
   p.counters = static_cast<int32_t*>(workspace_d);
