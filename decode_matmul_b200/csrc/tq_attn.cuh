@@ -21,9 +21,9 @@
 // about a tenth of their rate, and the one-row-per-key layout they take needs
 // no tensor map, so any page size and strides work.
 // Items (row, key head, head group) that a warp holds whole are written by
-// it.  The others leave partial (O, M, L): warps of a block join in shared
-// memory, blocks in global memory by the last block to arrive, in block order
-// (the same bits on every run).
+// it.  The others leave partial (O, M, L), which the last warp to arrive joins,
+// first inside the block, then over the blocks, in a fixed order (the same
+// bits on every run).
 #pragma once
 
 #include "tq_kv.cuh"
@@ -41,6 +41,9 @@ struct AttnParams {
   int32_t head_groups;  // items per key head
   int32_t min_units;    // units a block takes at least before another is used
   uint32_t page_mul, page_shift;  // j / page_size = (umulhi(j, mul) + j) >> shift
+  // the cache's strides in units of unit bytes (a power of two that divides
+  // them all), in which every offset fits 32 bits
+  uint32_t unit, page_step, token_step, head_step;
   float scale;
   int32_t out_bf16;
   int32_t* counters;
@@ -61,7 +64,7 @@ struct AttnCfg {
   static constexpr int COLS = 8 * NT;        // head columns
   static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
   static constexpr int SLOT = PART * 4;
-  static constexpr int CTL = 3072;
+  static constexpr int CTL = 2048;
   static constexpr int fit(int warps) { return ((227 * 1024 - CTL) / warps - SLOT) / STAGE; }
   // as many warps as leave each a ring of three tiles, else four
   static constexpr int WARPS = fit(8) >= 3 ? 8 : (fit(6) >= 3 ? 6 : 4);
@@ -112,10 +115,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t lo16) {
-  uint32_t r;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }\n" : "=r"(r) : "r"(lo16));
-  return r;
+// the four e4m3 values of a word as two fp16 pairs (exact)
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h; }\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 template <bool BF16>
 __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -146,7 +150,7 @@ constexpr int kItemCost = 2;
 
 // Where a warp stands in the tile order.
 struct AttnWalk {
-  int64_t row_at;        // first unit of the row in the whole call's order
+  int32_t row_at;        // first unit of the row in the whole call's order
   int32_t row, item, j;  // row, item in the row, tile in the item
   int32_t n;             // tiles of an item of this row
   AttnRow r;
@@ -163,10 +167,120 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int row, bool& 
   return r;
 }
 
-// a / b, without the long division where the values allow it
-__device__ __forceinline__ int64_t quot(int64_t a, int32_t b) {
-  return ((uint64_t)a >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
+// ---- join -----------------------------------------------------------------------
+// A part is (O, M, L) relative to its own maximum: O [D][COLS], M [COLS],
+// L [COLS].  Parts join to sum_i 2^(M_i - M) O_i.  When its warps are done a
+// block joins their parts of each item in shared memory.  Of an item that goes
+// beyond the block (at most its first and its last) it publishes the result,
+// and the last block to publish joins the blocks' parts; in groups of kJoin
+// when there are more, so that a row spread over the whole GPU takes two short
+// rounds.  No block waits for another.
+constexpr int kJoin = 16;
+constexpr int kTopCounters = 1024;  // counters of the second round (the first's are two per block)
+
+// The joined parts of one thread: QPT quads of O at quad u * THREADS + tid,
+// all of the same four columns col.
+template <int D, int COLS, int THREADS>
+struct AttnSum {
+  static constexpr int QUADS = D * COLS / 4;
+  static constexpr int QPT = (QUADS + THREADS - 1) / THREADS;
+  static constexpr bool FULL = QUADS % THREADS == 0;
+  static_assert((THREADS * 4) % COLS == 0, "columns");
+  float4 acc[QPT];
+  float M[4], L[4];
+
+  static __device__ __forceinline__ float weight(float m, float top) { return top == -INFINITY ? 0.f : ex2(m - top); }
+  static __device__ __forceinline__ int col() { return (threadIdx.x * 4) % COLS; }
+  static __device__ __forceinline__ bool in(int u) { return FULL || u * THREADS + (int)threadIdx.x < QUADS; }
+  static __device__ __forceinline__ int quad(int u) { return (u * THREADS + threadIdx.x) * 4; }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) M[k] = -INFINITY, L[k] = 0.f;
+#pragma unroll
+    for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // raises the maxima to cover m, scaling what has been summed
+  __device__ __forceinline__ void raise(float4 m) {
+    const float f[4] = {fmaxf(M[0], m.x), fmaxf(M[1], m.y), fmaxf(M[2], m.z), fmaxf(M[3], m.w)};
+    float r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      r[k] = weight(M[k], f[k]);
+      M[k] = f[k];
+      L[k] *= r[k];
+    }
+#pragma unroll
+    for (int u = 0; u < QPT; ++u) acc[u].x *= r[0], acc[u].y *= r[1], acc[u].z *= r[2], acc[u].w *= r[3];
+  }
+  // B parts at p(0) .. p(B-1), of which the first n count: their loads are in flight together
+  template <int B, class P>
+  __device__ __forceinline__ void add(int n, P p) {
+    float4 m[B], l[B], v[B][QPT];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      m[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < n) {
+        const float* src = p(i);
+        m[i] = *reinterpret_cast<const float4*>(src + D * COLS + col());
+        l[i] = *reinterpret_cast<const float4*>(src + D * COLS + COLS + col());
+#pragma unroll
+        for (int u = 0; u < QPT; ++u)
+          if (in(u)) v[i][u] = *reinterpret_cast<const float4*>(src + quad(u));
+      }
+    }
+    float4 top = m[0];
+#pragma unroll
+    for (int i = 1; i < B; ++i)
+      top = make_float4(fmaxf(top.x, m[i].x), fmaxf(top.y, m[i].y), fmaxf(top.z, m[i].z), fmaxf(top.w, m[i].w));
+    raise(top);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (i < n) {
+        const float f[4] = {weight(m[i].x, M[0]), weight(m[i].y, M[1]), weight(m[i].z, M[2]), weight(m[i].w, M[3])};
+        L[0] += f[0] * l[i].x, L[1] += f[1] * l[i].y, L[2] += f[2] * l[i].z, L[3] += f[3] * l[i].w;
+#pragma unroll
+        for (int u = 0; u < QPT; ++u)
+          if (in(u))
+            acc[u].x += f[0] * v[i][u].x, acc[u].y += f[1] * v[i][u].y, acc[u].z += f[2] * v[i][u].z,
+                acc[u].w += f[3] * v[i][u].w;
+      }
+  }
+  // n blocks' parts at p(0) .. p(n-1)
+  template <class P>
+  __device__ __forceinline__ void sum(int n, P p) {
+    constexpr int B = QPT == 1 ? 8 : (QPT <= 4 ? 4 : 2);
+    clear();
+#pragma unroll 1
+    for (int i = 0; i < n; i += B) add<B>(n - i, [&](int k) { return p(i + k); });
+  }
+  __device__ __forceinline__ void store(float* to) const {
+#pragma unroll
+    for (int u = 0; u < QPT; ++u)
+      if (in(u)) *reinterpret_cast<float4*>(to + quad(u)) = acc[u];
+    if (threadIdx.x < COLS / 4) {
+      *reinterpret_cast<float4*>(to + D * COLS + col()) = make_float4(M[0], M[1], M[2], M[3]);
+      *reinterpret_cast<float4*>(to + D * COLS + COLS + col()) = make_float4(L[0], L[1], L[2], L[3]);
+    }
+  }
+  // the item's rounded output
+  __device__ __forceinline__ void write(const AttnParams& p, int row, int item) const {
+    const int kvh = item / p.head_groups, h0 = (item - kvh * p.head_groups) * COLS + col();
+    const float vsc = p.c.vs ? p.c.vs[kvh] : 1.f;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + ((int64_t)row * p.q_heads + kvh * p.group + h0) * D;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (h0 + k >= p.group) continue;
+      const float inv = L[k] == 0.f ? 0.f : vsc / L[k];
+#pragma unroll
+      for (int u = 0; u < QPT; ++u)
+        if (in(u)) {
+          const float y = (k == 0 ? acc[u].x : k == 1 ? acc[u].y : k == 2 ? acc[u].z : acc[u].w) * inv;
+          out[k * D + quad(u) / COLS] = p.out_bf16 ? f_to_bf16_bits(y) : __half_as_ushort(__float2half_rn(y));
+        }
+    }
+  }
+};
 
 template <int TK>
 __device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int items) {
@@ -174,7 +288,7 @@ __device__ __forceinline__ void attn_next(const AttnParams& p, AttnWalk& w, int 
   w.j = 0;
   if (++w.item < items) return;
   w.item = 0;
-  w.row_at += (int64_t)(w.n + kItemCost) * items;
+  w.row_at += (w.n + kItemCost) * items;
   if (++w.row < p.m) {
     bool bad;
     w.r = attn_row(p, w.row, bad);
@@ -189,18 +303,14 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   constexpr bool F8 = T == KV_E4M3;
   constexpr int W = C::WARPS, S = C::STAGES, COLS = C::COLS, MT = D / 16, TK = C::TK, KT = C::KT;
   extern __shared__ __align__(16) uint8_t smem[];
-  struct Seg {
-    int64_t start;  // unit of the first tile of the segment's item
-    int32_t n, row, item;  // n: its tiles, 0 = no segment
-    int32_t pad;
+  struct Part {  // what a warp left in a slot
+    int32_t first, n, row, item;  // unit of the item's first tile, its tiles (0: nothing)
   };
   struct Ctl {
     int64_t warp_sum[W];
-    AttnWalk at[W];  // where each warp's range begins
-    Seg seg[2 * W];  // what warp w left in its head (2w) and tail (2w+1) slot
-    float weight[2 * W][COLS];  // of the parts of an item
-    float top[2][COLS];         // M and L of the joined parts
-    int32_t last;
+    AttnWalk at[W];    // where each warp's range begins
+    Part part[2 * W];  // warp w's head slot (2w) and tail slot (2w + 1)
+    int32_t last[2];
   };
   static_assert(sizeof(Ctl) <= C::CTL, "control block");
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + W * C::WARP_BYTES);
@@ -214,33 +324,42 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   // Up to 128 rows every warp sums them for itself (four rows per lane at most,
   // no barrier); more are shared among the block's threads.
   AttnWalk cw;  // where this warp stands
-  int64_t u0, u1;            // units of this warp
-  int64_t b0, total, share;  // block c takes share units, one more when c < rest
-  int32_t blocks, rest;
+  int32_t u0, u1;            // units of this warp
+  int32_t b0, share, rest, blocks;  // block c takes share units, one more when c < rest
+  int32_t wshare, wrest;            // and so its warps
+  // false: this block has nothing to do.  A call of 2^31 units (30 TB of
+  // keys and values and more) is refused.
   auto split = [&](int64_t rows_total) {
-    total = rows_total * items;
+    if (rows_total > 0x7fffffffll / items) {
+      if (tid == 0 && blockIdx.x == 0) flag_bad_index(p.status);
+      return false;
+    }
+    const int32_t total = (int32_t)rows_total * items, c = blockIdx.x;
     blocks = gridDim.x;
-    if (total < (int64_t)blocks * p.min_units) blocks = ((int32_t)total + p.min_units - 1) / p.min_units;
-    share = quot(total, blocks);
-    rest = (int32_t)(total - share * blocks);
-    const int32_t c = blockIdx.x;
+    if (total < blocks * p.min_units) blocks = (uint32_t)(total + p.min_units - 1) / (uint32_t)p.min_units;
+    share = (uint32_t)total / (uint32_t)blocks;
+    rest = total - share * blocks;
     b0 = c * share + (c < rest ? c : rest);
+    const int32_t len = share + (c < rest ? 1 : 0);
+    wshare = len / W;
+    wrest = len - wshare * W;
+    return c < blocks;
   };
-  // first unit of warp w (of the block's share: an even split again)
-  auto warp_first = [&](int w) {
-    const int64_t len = share + ((int32_t)blockIdx.x < rest ? 1 : 0);
-    const int64_t ls = quot(len, W);
-    const int32_t lr = (int32_t)(len - ls * W);
-    return b0 + w * ls + (w < lr ? w : lr);
+  auto warp_first = [&](int w) { return b0 + w * wshare + (w < wrest ? w : wrest); };
+  // the block whose share holds unit u
+  auto block_of = [&](int32_t u) {
+    const uint32_t lead = (uint32_t)rest * (share + 1);
+    return (uint32_t)u < lead ? (int32_t)((uint32_t)u / (uint32_t)(share + 1))
+                              : rest + (int32_t)(((uint32_t)u - lead) / (uint32_t)share);
   };
   // the first tile at or after unit o of the row (it may be in the next row)
-  auto place = [&](AttnWalk& w, int64_t o) {
+  auto place = [&](AttnWalk& w, int32_t o) {
     const int32_t unit = w.n + kItemCost;
-    w.item = (int32_t)quot(o, unit);
-    w.j = (int32_t)(o - (int64_t)w.item * unit) - kItemCost;
+    w.item = (uint32_t)o / (uint32_t)unit;
+    w.j = o - w.item * unit - kItemCost;
     if (w.j < 0) w.j = 0;
   };
-  if (tid < 2 * W) ctl->seg[tid].n = 0;
+  if (tid < 2 * W) ctl->part[tid].n = 0;
   if (p.m <= 128) {
     const int per = (p.m + 31) >> 5;
     AttnRow r[4];
@@ -265,17 +384,16 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       const int64_t v = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += v;
     }
-    split(__shfl_sync(0xffffffffu, incl, 31));
-    if ((int32_t)blockIdx.x >= blocks) return;
+    if (!split(__shfl_sync(0xffffffffu, incl, 31))) return;
     u0 = warp_first(warp);
     u1 = warp_first(warp + 1);
-    int64_t at = (incl - mine) * items;
-    const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= at && u0 < incl * items)) - 1;  // none when the range is empty
+    int32_t at = (int32_t)(incl - mine) * items;
+    const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= at && u0 < (int32_t)incl * items)) - 1;  // none when the range is empty
     const int sl = src < 0 ? 0 : src;
     AttnWalk w = {at, lane * per, 0, 0, n[0], r[0]};
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
-      at += (int64_t)(n[i - 1] ? n[i - 1] + kItemCost : 0) * items;
+      at += (n[i - 1] ? n[i - 1] + kItemCost : 0) * items;
       if (n[i] && u0 >= at) w = {at, lane * per + i, 0, 0, n[i], r[i]};
     }
     cw.row = __shfl_sync(0xffffffffu, w.row, sl);
@@ -310,11 +428,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       if (i < warp) before += ctl->warp_sum[i];
       rows_total += ctl->warp_sum[i];
     }
-    split(rows_total);
-    if ((int32_t)blockIdx.x >= blocks) return;
-    const int64_t b1 = warp_first(W);
-    int64_t at = (before + incl - mine) * items;  // first unit of row r0
-    if ((before + incl) * items > b0 && at < b1) {
+    if (!split(rows_total)) return;
+    const int32_t b1 = warp_first(W);
+    int32_t at = (int32_t)(before + incl - mine) * items;  // first unit of row r0
+    if ((int32_t)(before + incl) * items > b0 && at < b1) {
       for (int i = r0; i < r1; ++i) {
         AttnWalk w;
         bool bad;
@@ -322,9 +439,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         w.n = w.r.tiles<TK>();
         w.row = i;
         w.row_at = at;
-        at += (int64_t)(w.n + kItemCost) * items;
+        at += (w.n + kItemCost) * items;
         for (int k = 0; k < W; ++k) {
-          const int64_t s = warp_first(k);
+          const int32_t s = warp_first(k);
           if (s >= w.row_at && s < at) {
             place(w, s - w.row_at);
             ctl->at[k] = w;
@@ -338,7 +455,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     if (u0 < u1) cw = ctl->at[warp];
   }
   // unit of the tile that a walk stands at
-  auto unit_of = [&](const AttnWalk& w) { return w.row_at + (int64_t)w.item * (w.n + kItemCost) + kItemCost + w.j; };
+  auto unit_of = [&](const AttnWalk& w) { return w.row_at + w.item * (w.n + kItemCost) + kItemCost + w.j; };
 
   uint8_t* ring = smem + warp * C::WARP_BYTES;
   float* head_slot = reinterpret_cast<float*>(ring + C::RING);  // O of the first item when it began before the warp
@@ -350,58 +467,64 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     bool more = true;  // pw stands at a tile of this warp
 
     // look-up state of the producer: lane l < TK holds key l of the tile
-    int32_t page = 0;
-    int64_t off = 0;  // offset inside the page, head included
-    bool valid = false;
+    constexpr uint32_t FULL_MASK = 0xffffffffu >> (32 - TK);
+    struct Look {
+      int32_t page;
+      uint32_t off;  // offset inside the page, head included
+      bool valid;
+    };
     auto look = [&]() {
-      valid = false;
+      Look l = {-1, 0u, false};
       if (more) {
         const int32_t idx = pw.j * TK + (lane & (TK - 1));
         if (idx < pw.r.keys) {
           const uint32_t t = (uint32_t)(pw.r.first + idx);
           const uint32_t pi = (__umulhi(t, p.page_mul) + t) >> p.page_shift;
-          page = p.c.pages[(int64_t)pw.r.seq * p.c.max_pages + pi];
-          off = (int64_t)(t - pi * (uint32_t)p.c.page_size) * p.c.token_stride +
-                (int64_t)(pw.item / p.head_groups) * p.c.head_stride;
-          valid = true;
+          l.page = p.c.pages[(int64_t)pw.r.seq * p.c.max_pages + pi];
+          l.off = (t - pi * (uint32_t)p.c.page_size) * p.token_step + (uint32_t)(pw.item / p.head_groups) * p.head_step;
+          l.valid = true;
         }
         attn_next<TK>(p, pw, items);
         more = pw.row < p.m && unit_of(pw) < u1;
       }
+      return l;
     };
+    // a lane copies chunk lane % CPR of every (32 / CPR)-th key (rows of 12 and 6 chunks: any chunk)
+    constexpr bool EVEN = 32 % C::CPR == 0;
     uint64_t masks = 0;  // valid keys of the tiles in flight, TK bits each, the oldest highest
     int stage_in = 0;
-    auto copy = [&]() {  // start the copies of the looked-up tile
-      bool ok = valid;
-      if (ok && (page < 0 || page >= p.c.n_pages)) {
-        flag_bad_index(p.status);
-        ok = false;
-      }
-      const int64_t o = ok ? (int64_t)page * p.c.page_stride + off : -1;
-      const uint32_t vm = __ballot_sync(0xffffffffu, ok) & (0xffffffffu >> (32 - TK));
+    auto copy = [&](const Look& l) {  // start the copies of a looked-up tile
+      const bool ok = l.valid && l.page >= 0 && l.page < p.c.n_pages;
+      if (l.valid && !ok) flag_bad_index(p.status);
+      const uint32_t o = ok ? (uint32_t)l.page * p.page_step + l.off : 0u;
+      const uint32_t vm = __ballot_sync(0xffffffffu, ok) & FULL_MASK;
       masks = (masks << TK) | vm;
       if (vm) {
         const uint32_t base = ring_u + stage_in * C::STAGE;
 #pragma unroll
         for (int i = 0; i < C::CPR * TK / 32; ++i) {
           const int c = i * 32 + lane;
-          const int r = c / C::CPR, ch = c - r * C::CPR;
-          const int64_t ro = __shfl_sync(0xffffffffu, o, r);
-          const int64_t bo = (ro < 0 ? 0 : ro) * C::EB + ch * 16;
+          const int r = EVEN ? i * (32 / C::CPR) + lane / C::CPR : c / C::CPR;
+          const int ch = EVEN ? lane % C::CPR : c - r * C::CPR;
+          const uint64_t bo = (uint64_t)__shfl_sync(0xffffffffu, o, r) * p.unit + ch * 16;
           const uint32_t d = base + r * C::RB + (ch ^ C::swz(r)) * 16;
-          cp_async16(d, static_cast<const uint8_t*>(p.c.k) + (ro < 0 ? 0 : bo), ro >= 0);
-          cp_async16(d + TK * C::RB, static_cast<const uint8_t*>(p.c.v) + (ro < 0 ? 0 : bo), ro >= 0);
+          const bool in = vm == FULL_MASK || (vm >> r & 1);
+          cp_async16(d, static_cast<const uint8_t*>(p.c.k) + bo, in);
+          cp_async16(d + TK * C::RB, static_cast<const uint8_t*>(p.c.v) + bo, in);
         }
       }
       cp_async_commit();
       if (++stage_in == S) stage_in = 0;
     };
 
-    look();
+    Look next;
+    {
+      Look l[S - 1];  // the first look-ups together: their latencies overlap
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-      copy();
-      look();
+      for (int i = 0; i < S - 1; ++i) l[i] = look();
+      next = look();
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) copy(l[i]);
     }
 
     uint32_t qf[NT][MT][2];
@@ -424,6 +547,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         fresh = false;
         const int kvh = cw.item / p.head_groups;
         sc = p.scale * 1.44269504088896340736f * (p.c.ks ? p.c.ks[kvh] : 1.f);
+        // a negative scale turns the queries around, so that the largest product has the largest score
+        const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
+        sc = fabsf(sc);
         vscale = p.c.vs ? p.c.vs[kvh] : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -442,8 +568,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
                 x1 = *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8 + (lane & 3) * 2);
               }
             }
-            qf[nt][ks][0] = x0;
-            qf[nt][ks][1] = x1;
+            qf[nt][ks][0] = x0 ^ flip;
+            qf[nt][ks][1] = x1 ^ flip;
           }
           mx[nt][0] = mx[nt][1] = -INFINITY;
           sum[nt][0] = sum[nt][1] = 0.f;
@@ -457,8 +583,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       cp_async_wait<S - 2>();
       __syncwarp();
       const uint32_t vm = (uint32_t)(masks >> (TK * (S - 2))) & (0xffffffffu >> (32 - TK));
-      copy();  // into the stage that the previous tile has left
-      look();
+      copy(next);  // into the stage that the previous tile has left
+      next = look();
 
       if (vm) {
         const uint32_t kb = ring_u + stage_out * C::STAGE;
@@ -495,15 +621,17 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               ldsm4(r, ka + kt * 16 * C::RB + (kx ^ (ks * 16)));
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const uint32_t a[4] = {e4m3x2_to_h2(r[2 * u]), e4m3x2_to_h2(r[2 * u + 1]), e4m3x2_to_h2(r[2 * u] >> 16),
-                                       e4m3x2_to_h2(r[2 * u + 1] >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_h2(r[2 * u], a[0], a[2]);
+                e4m3x4_to_h2(r[2 * u + 1], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma16<BF>(u ? s2[kt][nt] : s[kt][nt], a, qf[nt][ks + u][0], qf[nt][ks + u][1]);
               }
             }
         }
-        // softmax: lane holds keys lane/4 and lane/4 + 8 (of each 16) of heads 2(lane%4) and +1
+        // softmax: lane holds keys lane/4 and lane/4 + 8 (of each 16) of heads
+        // 2(lane%4) and +1; mx is the largest product, weights 2^(sc (x - mx))
         float tm[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -513,12 +641,29 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                float& x = s[kt][nt][2 * r + i];
-                x = (vm >> (kt * 16 + r * 8 + (lane >> 2))) & 1 ? (x + s2[kt][nt][2 * r + i]) * sc : -INFINITY;
-                tm[nt][i] = fmaxf(tm[nt][i], x);
-              }
+              for (int r = 0; r < 2; ++r) s[kt][nt][2 * r + i] += s2[kt][nt][2 * r + i];
           }
+        if (vm != FULL_MASK) {
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const bool in = (vm >> (kt * 16 + r * 8 + (lane >> 2))) & 1;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (!in) s[kt][nt][2 * r + i] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) tm[nt][i] = fmaxf(tm[nt][i], s[kt][nt][2 * r + i]);
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
 #pragma unroll
@@ -536,7 +681,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float mn = fmaxf(mx[nt][i], tm[nt][i]);
-              const float f = mn == -INFINITY ? 1.f : ex2(mx[nt][i] - mn);
+              const float f = mx[nt][i] == -INFINITY ? 0.f : ex2((mx[nt][i] - mn) * sc);
               mx[nt][i] = mn;
               sum[nt][i] *= f;
 #pragma unroll
@@ -555,7 +700,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         for (int nt = 0; nt < NT; ++nt) {
           float m0[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) m0[i] = mx[nt][i] == -INFINITY ? 0.f : mx[nt][i];
+          for (int i = 0; i < 2; ++i) m0[i] = mx[nt][i] == -INFINITY ? 0.f : -mx[nt][i] * sc;
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -563,7 +708,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               float e[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                e[i] = ex2(s[kt][nt][2 * r + i] - m0[i]);
+                const float x = s[kt][nt][2 * r + i];
+                // x is -inf for hidden keys (and sc may be 0)
+                e[i] = vm == FULL_MASK || x != -INFINITY ? ex2(fmaf(x, sc, m0[i])) : 0.f;
                 sum[nt][i] += e[i];
               }
               if constexpr (BF) {
@@ -606,8 +753,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               ldsm4_t(r, va + kt * 16 * C::RB + (kx ^ (mt * 16)));
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                const uint32_t x = __byte_perm(r[2 * u], 0, 0x3120), y = __byte_perm(r[2 * u + 1], 0, 0x3120);
-                const uint32_t a[4] = {e4m3x2_to_h2(x), e4m3x2_to_h2(x >> 16), e4m3x2_to_h2(y), e4m3x2_to_h2(y >> 16)};
+                uint32_t a[4];
+                e4m3x4_to_h2(__byte_perm(r[2 * u], 0, 0x3120), a[0], a[1]);
+                e4m3x4_to_h2(__byte_perm(r[2 * u + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, ph[kt][nt][0], ph[kt][nt][1]);
               }
@@ -656,7 +804,6 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
             }
           }
         } else {
-          const int slot = item_end ? 0 : 1;
           if (!item_end) {
             cp_async_wait<0>();  // the ring is empty before its bytes are reused
             __syncwarp();
@@ -679,17 +826,13 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const int col = nt * 8 + lane * 2 + i;
-                dst[D * COLS + col] = mx[nt][i];
+                dst[D * COLS + col] = mx[nt][i] == -INFINITY ? -INFINITY : mx[nt][i] * sc;
                 dst[D * COLS + COLS + col] = sum[nt][i];
               }
           }
-          if (lane == 0) {
-            Seg& g = ctl->seg[2 * warp + slot];
-            g.start = tile.row_at + (int64_t)tile.item * (tile.n + kItemCost) + kItemCost;
-            g.n = tile.n;
-            g.row = tile.row;
-            g.item = tile.item;
-          }
+          if (lane == 0)
+            ctl->part[2 * warp + (item_end ? 0 : 1)] = {tile.row_at + tile.item * (tile.n + kItemCost) + kItemCost, tile.n,
+                                                        tile.row, tile.item};
         }
         began_before = false;
         fresh = true;
@@ -699,182 +842,86 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   }
   __syncthreads();
 
-  // ---- join: first the block's warps, then the blocks of an item ----------------
-  // parts: O, M, L relative to their own maxima; joined sum_i 2^(M_i - M) O_i
-  auto block_of = [&](int64_t tile) {
-    const int64_t lead = (int64_t)rest * (share + 1);
-    return tile < lead ? (int32_t)quot(tile, (int32_t)(share + 1)) : rest + (int32_t)quot(tile - lead, (int32_t)share);
-  };
-  constexpr int QUADS = D * COLS / 4;  // float4 of an O
-  constexpr int QPT = (QUADS + C::THREADS - 1) / C::THREADS;
-  constexpr bool FULL = QUADS % C::THREADS == 0;
-  constexpr int BATCH = QPT <= 2 ? 4 : 2;  // blocks' parts in flight together
-  const int col = (tid * 4) % COLS;  // the same for all of a thread's quads
-  static_assert((C::THREADS * 4) % COLS == 0, "columns");
-  float4 acc[QPT];
-  float M[4], L[4];
-  int64_t my_start = -1 - lane;
-  uint32_t live;
+  // ---- join (see AttnSum) -----------------------------------------------------------
+  const int32_t b1 = warp_first(W);
+  uint32_t live, same;  // slots with parts; of these, the ones of the same item
   {
-    const bool on = lane < 2 * W && ctl->seg[lane].n != 0;
-    if (on) my_start = ctl->seg[lane].start;
-    live = __ballot_sync(0xffffffffu, on);
+    const int32_t first = lane < 2 * W && ctl->part[lane].n ? ctl->part[lane].first : -1 - lane;
+    live = __ballot_sync(0xffffffffu, first >= 0);
+    same = __match_any_sync(0xffffffffu, first);
   }
-  const uint32_t same = __match_any_sync(0xffffffffu, (unsigned long long)my_start);
-  while (live) {  // the same in every warp
-    const int first = __ffs(live) - 1;
-    const uint32_t parts = __shfl_sync(0xffffffffu, same, first);
+  AttnSum<D, COLS, C::THREADS> sum;
+  auto global = [&](int c, bool second) { return p.partials + ((int64_t)c * 2 + second) * C::PART; };
+  Part beyond[2];  // the item that began before this block, and the one that goes on behind it
+  beyond[0].n = beyond[1].n = 0;
+  while (live) {  // the same in all warps
+    const int k0 = __ffs(live) - 1;
+    uint32_t parts = __shfl_sync(0xffffffffu, same, k0);
     live &= ~parts;
-    const Seg g = ctl->seg[first];
-    const int c_first = block_of(g.start), c_last = block_of(g.start + g.n - 1);
-    auto slot = [&](int k) {
-      const uint8_t* b = smem + (k >> 1) * C::WARP_BYTES;
-      return reinterpret_cast<const float*>((k & 1) ? b : b + C::RING);
-    };
-    auto weight = [&](float m, float top) { return top == -INFINITY ? 0.f : ex2(m - top); };
-    // the parts' weights: a lane per part, a half warp per column
-    for (int c = warp * 2 + (lane >> 4); c < COLS; c += 2 * W) {
-      const int k = lane & 15;
-      const bool in = k < 2 * W && (parts >> k & 1);
-      const float m = in ? slot(k)[D * COLS + c] : -INFINITY;
-      float l = in ? slot(k)[D * COLS + COLS + c] : 0.f, top = m;
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      const float f = in ? weight(m, top) : 0.f;
-      l *= f;
-#pragma unroll
-      for (int d = 1; d < 16; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-      if (in) ctl->weight[k][c] = f;
-      if (k == 0) {
-        ctl->top[0][c] = top;
-        ctl->top[1][c] = l;
-      }
+    const Part g = ctl->part[k0];
+    sum.clear();
+#pragma unroll 1
+    while (parts) {
+      const int ka = __ffs(parts) - 1;
+      parts &= parts - 1;
+      const int kb = parts ? __ffs(parts) - 1 : ka;
+      const int n = parts ? 2 : 1;
+      parts &= parts - 1;
+      sum.template add<2>(n, [&](int i) {
+        const int k = i ? kb : ka;
+        return reinterpret_cast<const float*>(smem + (k >> 1) * C::WARP_BYTES + ((k & 1) ? 0 : C::RING));
+      });
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      M[k] = ctl->top[0][col + k];
-      L[k] = ctl->top[1][col + k];
+    if (g.first >= b0 && g.first + g.n <= b1) {
+      sum.write(p, g.row, g.item);
+    } else {
+      // the second slot is for the item that begins in this block
+      const bool second = g.first >= b0;
+      sum.store(global(blockIdx.x, second));
+      beyond[second] = g;
     }
-#pragma unroll
-    for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t rem = parts; rem;) {
-      // four parts at a time, the bits of rem in order
-      const float* part[4];
-      float4 f[4];
-      bool on[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        on[i] = rem != 0;
-        const int k = on[i] ? __ffs(rem) - 1 : first;
-        part[i] = slot(k);
-        f[i] = *reinterpret_cast<const float4*>(&ctl->weight[k][col]);
-        rem &= rem - 1;
-      }
-#pragma unroll
-      for (int u = 0; u < QPT; ++u) {
-        const int qd = u * C::THREADS + tid;
-        if (FULL || qd < QUADS) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (!on[i]) break;
-            const float4 v = *reinterpret_cast<const float4*>(part[i] + qd * 4);
-            acc[u].x += f[i].x * v.x, acc[u].y += f[i].y * v.y, acc[u].z += f[i].z * v.z, acc[u].w += f[i].w * v.w;
-          }
-        }
-      }
-    }
-    __syncthreads();  // the weights are read before the next item's are written
-    if (c_first != c_last) {
-      // publish the block's part; the last block of the item to arrive joins all of them, in block order
-      float* gp = p.partials + ((int64_t)blockIdx.x * 2 + (c_first == (int)blockIdx.x)) * C::PART;
-#pragma unroll
-      for (int u = 0; u < QPT; ++u) {
-        const int qd = u * C::THREADS + tid;
-        if (FULL || qd < QUADS) *reinterpret_cast<float4*>(gp + qd * 4) = acc[u];
-      }
-      if (tid < COLS / 4) {
-        *reinterpret_cast<float4*>(gp + D * COLS + col) = make_float4(M[0], M[1], M[2], M[3]);
-        *reinterpret_cast<float4*>(gp + D * COLS + COLS + col) = make_float4(L[0], L[1], L[2], L[3]);
-      }
+  }
+  if (beyond[0].n == 0 && beyond[1].n == 0) return;
+  __syncthreads();
+  // the blocks of an item are ca .. ca + n - 1; its part in block c is global(c, c == ca)
+  auto arrive = [&](int32_t* counter, int n) {  // in one thread: true for the last of n
+    const int32_t old = atomicAdd(counter, 1);
+    if (old == n - 1) *counter = 0;
+    return old == n - 1;
+  };
+  if (tid < 2) {
+    const Part g = tid ? beyond[1] : beyond[0];
+    ctl->last[tid] = 0;
+    if (g.n) {
+      const int ca = block_of(g.first), n = block_of(g.first + g.n - 1) - ca + 1;
+      const int i0 = ((int)blockIdx.x - ca) / kJoin * kJoin;  // its group's first block
       __threadfence();
-      __syncthreads();
-      if (tid == 0) ctl->last = atomicAdd(p.counters + c_first, 1) == c_last - c_first;
-      __syncthreads();
-      const bool last = ctl->last != 0;
-      __syncthreads();  // read by all before the next item's write
-      if (!last) continue;
+      ctl->last[tid] = arrive(p.counters + 2 * (ca + i0) + (i0 == 0), n - i0 < kJoin ? n - i0 : kJoin);
       __threadfence();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        M[k] = -INFINITY;
-        L[k] = 0.f;
-      }
-#pragma unroll
-      for (int u = 0; u < QPT; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = c_first; c <= c_last; c += BATCH) {
-        float4 m[BATCH], l[BATCH], v[BATCH][QPT];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          // past the end: a part of weight zero
-          m[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          l[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int u = 0; u < QPT; ++u) v[i][u] = l[i];
-          if (c + i <= c_last) {
-            const float* part = p.partials + ((int64_t)(c + i) * 2 + (c + i == c_first)) * C::PART;
-            m[i] = __ldcg(reinterpret_cast<const float4*>(part + D * COLS + col));
-            l[i] = __ldcg(reinterpret_cast<const float4*>(part + D * COLS + COLS + col));
-#pragma unroll
-            for (int u = 0; u < QPT; ++u) {
-              const int qd = u * C::THREADS + tid;
-              if (FULL || qd < QUADS) v[i][u] = __ldcg(reinterpret_cast<const float4*>(part + qd * 4));
-            }
-          }
-        }
-        float old[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) old[k] = M[k];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i)
-          M[0] = fmaxf(M[0], m[i].x), M[1] = fmaxf(M[1], m[i].y), M[2] = fmaxf(M[2], m[i].z), M[3] = fmaxf(M[3], m[i].w);
-        float r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          r[k] = weight(old[k], M[k]);
-          L[k] *= r[k];
-        }
-#pragma unroll
-        for (int u = 0; u < QPT; ++u) acc[u].x *= r[0], acc[u].y *= r[1], acc[u].z *= r[2], acc[u].w *= r[3];
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const float f[4] = {weight(m[i].x, M[0]), weight(m[i].y, M[1]), weight(m[i].z, M[2]), weight(m[i].w, M[3])};
-          L[0] += f[0] * l[i].x, L[1] += f[1] * l[i].y, L[2] += f[2] * l[i].z, L[3] += f[3] * l[i].w;
-#pragma unroll
-          for (int u = 0; u < QPT; ++u)
-            acc[u].x += f[0] * v[i][u].x, acc[u].y += f[1] * v[i][u].y, acc[u].z += f[2] * v[i][u].z,
-                acc[u].w += f[3] * v[i][u].w;
-        }
-      }
-      if (tid == 0) p.counters[c_first] = 0;
     }
-    const int kvh = g.item / p.head_groups, g0 = (g.item - kvh * p.head_groups) * COLS + col;
-    const float vsc = p.c.vs ? p.c.vs[kvh] : 1.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (g0 + k >= p.group) continue;
-      const float inv = L[k] == 0.f ? 0.f : vsc / L[k];
-      const int64_t at = ((int64_t)g.row * p.q_heads + kvh * p.group + g0 + k) * D;
-#pragma unroll
-      for (int u = 0; u < QPT; ++u) {
-        const int qd = u * C::THREADS + tid;
-        if (!FULL && qd >= QUADS) continue;
-        const float y = (k == 0 ? acc[u].x : k == 1 ? acc[u].y : k == 2 ? acc[u].z : acc[u].w) * inv;
-        const int d = qd * 4 / COLS;
-        static_cast<uint16_t*>(p.out)[at + d] =
-            p.out_bf16 ? f_to_bf16_bits(y) : __half_as_ushort(__float2half_rn(y));
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int s = 0; s < 2; ++s) {
+    if (!ctl->last[s]) continue;  // the same in all threads
+    const Part g = s ? beyond[1] : beyond[0];
+    const int ca = block_of(g.first), n = block_of(g.first + g.n - 1) - ca + 1;
+    const int i0 = ((int)blockIdx.x - ca) / kJoin * kJoin;
+    sum.sum(n - i0 < kJoin ? n - i0 : kJoin, [&](int i) { return global(ca + i0 + i, i0 + i == 0); });
+    if (n > kJoin) {
+      __syncthreads();  // every thread has read the group's parts, of which the first is replaced
+      sum.store(global(ca + i0, i0 == 0));
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        ctl->last[s] = arrive(p.counters + kTopCounters + ca, (n + kJoin - 1) / kJoin);
+        __threadfence();
       }
+      __syncthreads();
+      if (!ctl->last[s]) continue;
+      sum.sum((n + kJoin - 1) / kJoin, [&](int i) { return global(ca + i * kJoin, i == 0); });
     }
+    sum.write(p, g.row, g.item);
   }
 }
 

@@ -89,6 +89,24 @@ void divider(uint32_t d, uint32_t* mul, uint32_t* shift) {
   *shift = l;
 }
 
+// The cache's strides as 32-bit multiples of the largest power of two (4 KB at
+// most) that divides them; false when its last element is beyond 32 bits of them.
+bool attn_steps(const tq_kv_cache_t* c, tq::AttnParams* p) {
+  const int64_t eb = c->dtype == TQ_E4M3 ? 1 : 2;
+  const int64_t ps = c->page_stride * eb, ts = c->token_stride * eb, hs = c->head_stride * eb;
+  int64_t unit = 4096;
+  while ((ps | ts | hs) & (unit - 1)) unit >>= 1;
+  // products of the sizes with the strides, in units, checked without overflow
+  const double last = ((double)(c->n_pages - 1) * (double)ps + (double)(c->page_size - 1) * (double)ts +
+                       (double)(c->kv_heads - 1) * (double)hs) / (double)unit;
+  if (last > 4294967295.0 || ps / unit > 0xffffffffll || ts / unit > 0xffffffffll || hs / unit > 0xffffffffll) return false;
+  p->unit = (uint32_t)unit;
+  p->page_step = (uint32_t)(ps / unit);
+  p->token_step = (uint32_t)(ts / unit);
+  p->head_step = (uint32_t)(hs / unit);
+  return true;
+}
+
 template <int T, int D, int NT>
 int attn_launch(const tq::AttnParams& p, int sms, cudaStream_t stream) {
   using C = tq::AttnCfg<T, D, NT>;
@@ -204,6 +222,8 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   if (st != TQ_OK) return st;
   if (out_dtype != TQ_F16 && out_dtype != TQ_BF16) return TQ_ERR_VALUE;
   if (!isfinite(scale) || window < 0) return TQ_ERR_VALUE;
+  tq::AttnParams p;
+  if (!attn_steps(cache, &p)) return TQ_ERR_SHAPE;
   if (m == 0) return TQ_OK;
   if (!q_d || !pos_d || !out_d) return TQ_ERR_NULL;
   if (!aligned16(q_d) || !aligned16(out_d) || !aligned_to(pos_d, 4) || !aligned_to(seq_d, 4)) return TQ_ERR_ALIGN;
@@ -212,7 +232,6 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   int sms = 0;
   st = check_arch(&sms);
   if (st != TQ_OK) return st;
-  tq::AttnParams p;
   p.c = cache_view(cache);
   p.q = q_d;
   p.seq = seq_d;

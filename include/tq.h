@@ -435,7 +435,9 @@ TQ_API int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t 
                         const int32_t* seq_d, const int32_t* pos_d, const double* freq_d, int32_t rot_dim,
                         int32_t interleaved, void* q_out_d, void* workspace_d, size_t ws_bytes, void* stream);
 
-/* Attention of m new tokens over the cache.  Row t (query heads q_d[t]) sees
+/* Attention of m new tokens over the cache, which may span 2^32 times the
+ * largest power of two (4 KB at most) that divides its strides: 64 GB at the
+ * least, far more with whole pages of a power of two (TQ_ERR_SHAPE beyond).  Row t (query heads q_d[t]) sees
  * the keys j of sequence seq_d[t] (NULL: t) with j <= pos_d[t], and
  * j > pos_d[t] - window when window > 0.  Query head h reads key head
  * h / (q_heads / kv_heads):
