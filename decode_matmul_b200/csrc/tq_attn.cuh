@@ -39,6 +39,7 @@ struct AttnParams {
   int32_t m, q_heads, window;
   int32_t group;        // query heads per key head
   int32_t head_groups;  // items per key head
+  int32_t team;         // warps that work on neighbouring items over the same keys
   int32_t min_units;    // units a block takes at least before another is used
   uint32_t page_mul, page_shift;  // j / page_size = (umulhi(j, mul) + j) >> shift
   // the cache's strides in units of unit bytes (a power of two that divides
@@ -47,7 +48,7 @@ struct AttnParams {
   float scale;
   int32_t out_bf16;
   int32_t* counters;
-  float* partials;  // [grid][2][AttnCfg::PART]
+  float* partials;  // [grid][2][kTeamMax][AttnCfg::PART]
   int32_t* status;
 };
 
@@ -148,7 +149,14 @@ struct AttnRow {
 // 8192 keys: the slowest block took 1.35 times the mean without it).
 constexpr int kItemCost = 2;
 
-// Where a warp stands in the tile order.
+// Items next to each other in a row can be worked on by a team of warps, one
+// item each over the same keys: where a key of one head is less than 256 bytes
+// and its neighbours are other heads' (16 rows of 20000 to 65536 e4m3 keys of
+// 8 x 128 bytes: 268 us one by one, the same with the heads apart in memory
+// 219 us), and for two groups of query heads on one key head.
+constexpr int kTeamMax = 4;
+
+// Where a warp stands in the tile order (an item here is a team's items).
 struct AttnWalk {
   int32_t row_at;        // first unit of the row in the whole call's order
   int32_t row, item, j;  // row, item in the row, tile in the item
@@ -171,12 +179,12 @@ __device__ __forceinline__ AttnRow attn_row(const AttnParams& p, int row, bool& 
 // A part is (O, M, L) relative to its own maximum: O [D][COLS], M [COLS],
 // L [COLS].  Parts join to sum_i 2^(M_i - M) O_i.  When its warps are done a
 // block joins their parts of each item in shared memory.  Of an item that goes
-// beyond the block (at most its first and its last) it publishes the result,
-// and the last block to publish joins the blocks' parts; in groups of kJoin
+// beyond the block (at most its first and its last per team member) it publishes the result,
+// and the last block to publish joins the blocks' parts, in groups of kJoin
 // when there are more, so that a row spread over the whole GPU takes two short
 // rounds.  No block waits for another.
 constexpr int kJoin = 16;
-constexpr int kTopCounters = 1024;  // counters of the second round (the first's are two per block)
+constexpr int kTopCounters = 4096;  // counters of the second round (the first's are 2 kTeamMax per block)
 
 // The joined parts of one thread: QPT quads of O at quad u * THREADS + tid,
 // all of the same four columns col.
@@ -305,17 +313,20 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   extern __shared__ __align__(16) uint8_t smem[];
   struct Part {  // what a warp left in a slot
     int32_t first, n, row, item;  // unit of the item's first tile, its tiles (0: nothing)
+    int32_t member;
   };
   struct Ctl {
     int64_t warp_sum[W];
-    AttnWalk at[W];    // where each warp's range begins
+    AttnWalk at[W];    // where each team's range begins
     Part part[2 * W];  // warp w's head slot (2w) and tail slot (2w + 1)
-    int32_t last[2];
+    Part beyond[2][kTeamMax];  // items that began before this block; items that go on behind it
+    int32_t last[2 * kTeamMax];
   };
   static_assert(sizeof(Ctl) <= C::CTL, "control block");
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + W * C::WARP_BYTES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int items = p.c.kv_heads * p.head_groups;
+  const int team = p.team, items = p.c.kv_heads * p.head_groups / team;  // items: of a team
+  const int teams = W / team, my_team = warp / team, member = warp - my_team * team;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   AttnWalk cw;  // where this warp stands
   int32_t u0, u1;            // units of this warp
   int32_t b0, share, rest, blocks;  // block c takes share units, one more when c < rest
-  int32_t wshare, wrest;            // and so its warps
+  int32_t wshare, wrest;            // and so its teams
   // false: this block has nothing to do.  A call of 2^31 units (30 TB of
   // keys and values and more) is refused.
   auto split = [&](int64_t rows_total) {
@@ -341,11 +352,11 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     rest = total - share * blocks;
     b0 = c * share + (c < rest ? c : rest);
     const int32_t len = share + (c < rest ? 1 : 0);
-    wshare = len / W;
-    wrest = len - wshare * W;
+    wshare = len / teams;
+    wrest = len - wshare * teams;
     return c < blocks;
   };
-  auto warp_first = [&](int w) { return b0 + w * wshare + (w < wrest ? w : wrest); };
+  auto team_first = [&](int w) { return b0 + w * wshare + (w < wrest ? w : wrest); };
   // the block whose share holds unit u
   auto block_of = [&](int32_t u) {
     const uint32_t lead = (uint32_t)rest * (share + 1);
@@ -360,6 +371,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     if (w.j < 0) w.j = 0;
   };
   if (tid < 2 * W) ctl->part[tid].n = 0;
+  if (tid < 2 * kTeamMax) ctl->beyond[tid / kTeamMax][tid % kTeamMax].n = 0;
   if (p.m <= 128) {
     const int per = (p.m + 31) >> 5;
     AttnRow r[4];
@@ -385,8 +397,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       if (lane >= d) incl += v;
     }
     if (!split(__shfl_sync(0xffffffffu, incl, 31))) return;
-    u0 = warp_first(warp);
-    u1 = warp_first(warp + 1);
+    u0 = team_first(my_team);
+    u1 = team_first(my_team + 1);
     int32_t at = (int32_t)(incl - mine) * items;
     const int src = __ffs(__ballot_sync(0xffffffffu, u0 >= at && u0 < (int32_t)incl * items)) - 1;  // none when the range is empty
     const int sl = src < 0 ? 0 : src;
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       rows_total += ctl->warp_sum[i];
     }
     if (!split(rows_total)) return;
-    const int32_t b1 = warp_first(W);
+    const int32_t b1 = team_first(teams);
     int32_t at = (int32_t)(before + incl - mine) * items;  // first unit of row r0
     if ((int32_t)(before + incl) * items > b0 && at < b1) {
       for (int i = r0; i < r1; ++i) {
@@ -440,8 +452,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         w.row = i;
         w.row_at = at;
         at += (w.n + kItemCost) * items;
-        for (int k = 0; k < W; ++k) {
-          const int32_t s = warp_first(k);
+        for (int k = 0; k < teams; ++k) {
+          const int32_t s = team_first(k);
           if (s >= w.row_at && s < at) {
             place(w, s - w.row_at);
             ctl->at[k] = w;
@@ -450,9 +462,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
       }
     }
     __syncthreads();
-    u0 = warp_first(warp);
-    u1 = warp_first(warp + 1);
-    if (u0 < u1) cw = ctl->at[warp];
+    u0 = team_first(my_team);
+    u1 = team_first(my_team + 1);
+    if (u0 < u1) cw = ctl->at[my_team];
   }
   // unit of the tile that a walk stands at
   auto unit_of = [&](const AttnWalk& w) { return w.row_at + w.item * (w.n + kItemCost) + kItemCost + w.j; };
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
           const uint32_t t = (uint32_t)(pw.r.first + idx);
           const uint32_t pi = (__umulhi(t, p.page_mul) + t) >> p.page_shift;
           l.page = p.c.pages[(int64_t)pw.r.seq * p.c.max_pages + pi];
-          l.off = (t - pi * (uint32_t)p.c.page_size) * p.token_step + (uint32_t)(pw.item / p.head_groups) * p.head_step;
+          l.off = (t - pi * (uint32_t)p.c.page_size) * p.token_step + (uint32_t)((pw.item * team + member) / p.head_groups) * p.head_step;
           l.valid = true;
         }
         attn_next<TK>(p, pw, items);
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     for (bool done = false; !done;) {
       if (fresh) {
         fresh = false;
-        const int kvh = cw.item / p.head_groups;
+        const int item = cw.item * team + member, kvh = item / p.head_groups;
         sc = p.scale * 1.44269504088896340736f * (p.c.ks ? p.c.ks[kvh] : 1.f);
         // a negative scale turns the queries around, so that the largest product has the largest score
         const uint32_t flip = sc < 0.f ? 0x80008000u : 0u;
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
         vscale = p.c.vs ? p.c.vs[kvh] : 1.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int h = head_of(cw.item, nt * 8 + (lane >> 2));
+          const int h = head_of(item, nt * 8 + (lane >> 2));
           const uint16_t* qp = static_cast<const uint16_t*>(p.q) + ((int64_t)cw.row * p.q_heads + (h < 0 ? 0 : h)) * D;
 #pragma unroll
           for (int ks = 0; ks < MT; ++ks) {
@@ -784,7 +796,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
             float inv[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) inv[i] = sum[nt][i] == 0.f ? 0.f : vscale / sum[nt][i];
-            const int h = head_of(tile.item, nt * 8 + (lane >> 2));
+            const int h = head_of(tile.item * team + member, nt * 8 + (lane >> 2));
             uint16_t* op = static_cast<uint16_t*>(p.out) + ((int64_t)tile.row * p.q_heads + (h < 0 ? 0 : h)) * D;
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -832,7 +844,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
           }
           if (lane == 0)
             ctl->part[2 * warp + (item_end ? 0 : 1)] = {tile.row_at + tile.item * (tile.n + kItemCost) + kItemCost, tile.n,
-                                                        tile.row, tile.item};
+                                                        tile.row, tile.item * team + member, member};
         }
         began_before = false;
         fresh = true;
@@ -843,17 +855,20 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   __syncthreads();
 
   // ---- join (see AttnSum) -----------------------------------------------------------
-  const int32_t b1 = warp_first(W);
+  const int32_t b1 = team_first(teams);
   uint32_t live, same;  // slots with parts; of these, the ones of the same item
   {
-    const int32_t first = lane < 2 * W && ctl->part[lane].n ? ctl->part[lane].first : -1 - lane;
-    live = __ballot_sync(0xffffffffu, first >= 0);
-    same = __match_any_sync(0xffffffffu, first);
+    int32_t id = -1 - lane;
+    if (lane < 2 * W && ctl->part[lane].n) id = ctl->part[lane].row * items * team + ctl->part[lane].item;
+    live = __ballot_sync(0xffffffffu, id >= 0);
+    same = __match_any_sync(0xffffffffu, id);
   }
   AttnSum<D, COLS, C::THREADS> sum;
-  auto global = [&](int c, bool second) { return p.partials + ((int64_t)c * 2 + second) * C::PART; };
-  Part beyond[2];  // the item that began before this block, and the one that goes on behind it
-  beyond[0].n = beyond[1].n = 0;
+  // part of an item in block c: the second set of slots if the item begins there
+  auto global = [&](int c, bool second, int mem) {
+    return p.partials + (((int64_t)c * 2 + second) * kTeamMax + mem) * C::PART;
+  };
+  bool any = false;
   while (live) {  // the same in all warps
     const int k0 = __ffs(live) - 1;
     uint32_t parts = __shfl_sync(0xffffffffu, same, k0);
@@ -875,51 +890,56 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     if (g.first >= b0 && g.first + g.n <= b1) {
       sum.write(p, g.row, g.item);
     } else {
-      // the second slot is for the item that begins in this block
+      any = true;
       const bool second = g.first >= b0;
-      sum.store(global(blockIdx.x, second));
-      beyond[second] = g;
+      sum.store(global(blockIdx.x, second, g.member));
+      if (tid == 0) ctl->beyond[second][g.member] = g;
     }
   }
-  if (beyond[0].n == 0 && beyond[1].n == 0) return;
+  if (!any) return;
   __syncthreads();
-  // the blocks of an item are ca .. ca + n - 1; its part in block c is global(c, c == ca)
   auto arrive = [&](int32_t* counter, int n) {  // in one thread: true for the last of n
     const int32_t old = atomicAdd(counter, 1);
     if (old == n - 1) *counter = 0;
     return old == n - 1;
   };
-  if (tid < 2) {
-    const Part g = tid ? beyond[1] : beyond[0];
+  // the blocks of an item: ca .. ca + n - 1
+  auto extent = [&](const Part& g, int& ca, int& n) {
+    ca = block_of(g.first);
+    n = block_of(g.first + g.n - 1) - ca + 1;
+    return ((int)blockIdx.x - ca) / kJoin * kJoin;  // first of this block's group
+  };
+  if (tid < 2 * kTeamMax) {
+    const Part g = ctl->beyond[tid / kTeamMax][tid % kTeamMax];
     ctl->last[tid] = 0;
     if (g.n) {
-      const int ca = block_of(g.first), n = block_of(g.first + g.n - 1) - ca + 1;
-      const int i0 = ((int)blockIdx.x - ca) / kJoin * kJoin;  // its group's first block
+      int ca, n;
+      const int i0 = extent(g, ca, n);
       __threadfence();
-      ctl->last[tid] = arrive(p.counters + 2 * (ca + i0) + (i0 == 0), n - i0 < kJoin ? n - i0 : kJoin);
+      ctl->last[tid] = arrive(p.counters + (2 * (ca + i0) + (i0 == 0)) * kTeamMax + g.member, n - i0 < kJoin ? n - i0 : kJoin);
       __threadfence();
     }
   }
   __syncthreads();
 #pragma unroll 1
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < 2 * kTeamMax; ++s) {
     if (!ctl->last[s]) continue;  // the same in all threads
-    const Part g = s ? beyond[1] : beyond[0];
-    const int ca = block_of(g.first), n = block_of(g.first + g.n - 1) - ca + 1;
-    const int i0 = ((int)blockIdx.x - ca) / kJoin * kJoin;
-    sum.sum(n - i0 < kJoin ? n - i0 : kJoin, [&](int i) { return global(ca + i0 + i, i0 + i == 0); });
+    const Part g = ctl->beyond[s / kTeamMax][s % kTeamMax];
+    int ca, n;
+    const int i0 = extent(g, ca, n);
+    sum.sum(n - i0 < kJoin ? n - i0 : kJoin, [&](int i) { return global(ca + i0 + i, i0 + i == 0, g.member); });
     if (n > kJoin) {
       __syncthreads();  // every thread has read the group's parts, of which the first is replaced
-      sum.store(global(ca + i0, i0 == 0));
+      sum.store(global(ca + i0, i0 == 0, g.member));
       __syncthreads();
       if (tid == 0) {
         __threadfence();
-        ctl->last[s] = arrive(p.counters + kTopCounters + ca, (n + kJoin - 1) / kJoin);
+        ctl->last[s] = arrive(p.counters + kTopCounters + ca * kTeamMax + g.member, (n + kJoin - 1) / kJoin);
         __threadfence();
       }
       __syncthreads();
       if (!ctl->last[s]) continue;
-      sum.sum((n + kJoin - 1) / kJoin, [&](int i) { return global(ca + i * kJoin, i == 0); });
+      sum.sum((n + kJoin - 1) / kJoin, [&](int i) { return global(ca + i * kJoin, i == 0, g.member); });
     }
     sum.write(p, g.row, g.item);
   }

@@ -77,7 +77,7 @@ int attn_cols(const tq_kv_cache_t* c, int32_t q_heads) { return q_heads / c->kv_
 
 size_t attn_ws_bytes(const tq_kv_cache_t* c, int32_t q_heads) {
   const int cols = attn_cols(c, q_heads);
-  return kCounterBytes + (size_t)kAttnMaxBlocks * 2 * (c->head_dim * cols + 2 * cols) * sizeof(float);
+  return kCounterBytes + (size_t)kAttnMaxBlocks * 2 * tq::kTeamMax * (c->head_dim * cols + 2 * cols) * sizeof(float);
 }
 
 // Multiplier and shift of an exact division of values below 2^31 by d:
@@ -107,8 +107,24 @@ bool attn_steps(const tq_kv_cache_t* c, tq::AttnParams* p) {
   return true;
 }
 
+// Warps that work together on neighbouring items (tq_attn.cuh): enough that
+// their keys make 256 bytes in a row, or that all query heads of a key head are
+// among them; a power of two that divides the items and the block's warps.
+int attn_team(const tq_kv_cache_t* c, int head_groups, int warps) {
+  const int row = c->head_dim * (c->dtype == TQ_E4M3 ? 1 : 2);
+  int want = 1;
+  while (want < head_groups) want *= 2;
+  if (c->head_stride == c->head_dim && c->page_size > 1)
+    while (want * row < 256) want *= 2;
+  int team = 1;
+  while (2 * team <= want && 2 * team <= tq::kTeamMax && (c->kv_heads * head_groups) % (2 * team) == 0 &&
+         warps % (2 * team) == 0)
+    team *= 2;
+  return team;
+}
+
 template <int T, int D, int NT>
-int attn_launch(const tq::AttnParams& p, int sms, cudaStream_t stream) {
+int attn_launch(tq::AttnParams p, const tq_kv_cache_t* c, int sms, cudaStream_t stream) {
   using C = tq::AttnCfg<T, D, NT>;
   auto kern = tq::attn_kernel<T, D, NT>;
   static int configured[kMaxDevices];
@@ -118,22 +134,23 @@ int attn_launch(const tq::AttnParams& p, int sms, cudaStream_t stream) {
     TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM));
     configured[dev] = 1;
   }
+  p.team = attn_team(c, p.head_groups, C::WARPS);
   const int grid = sms < kAttnMaxBlocks ? sms : kAttnMaxBlocks;
   return launch(kern, dim3((unsigned)grid), dim3(C::THREADS), C::SMEM, stream, p);
 }
 
 template <int T, int D>
-int attn_launch_d(const tq::AttnParams& p, int cols, int sms, cudaStream_t stream) {
-  return cols == 8 ? attn_launch<T, D, 1>(p, sms, stream) : attn_launch<T, D, 2>(p, sms, stream);
+int attn_launch_d(const tq::AttnParams& p, const tq_kv_cache_t* c, int cols, int sms, cudaStream_t stream) {
+  return cols == 8 ? attn_launch<T, D, 1>(p, c, sms, stream) : attn_launch<T, D, 2>(p, c, sms, stream);
 }
 
 template <int T>
-int attn_launch_t(const tq::AttnParams& p, int cols, int sms, cudaStream_t stream) {
+int attn_launch_t(const tq::AttnParams& p, const tq_kv_cache_t* c, int cols, int sms, cudaStream_t stream) {
   switch (p.c.head_dim) {
-    case 64: return attn_launch_d<T, 64>(p, cols, sms, stream);
-    case 96: return attn_launch_d<T, 96>(p, cols, sms, stream);
-    case 128: return attn_launch_d<T, 128>(p, cols, sms, stream);
-    default: return attn_launch_d<T, 256>(p, cols, sms, stream);
+    case 64: return attn_launch_d<T, 64>(p, c, cols, sms, stream);
+    case 96: return attn_launch_d<T, 96>(p, c, cols, sms, stream);
+    case 128: return attn_launch_d<T, 128>(p, c, cols, sms, stream);
+    default: return attn_launch_d<T, 256>(p, c, cols, sms, stream);
   }
 }
 
@@ -252,9 +269,9 @@ int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32_t q_he
   p.status = status_word(workspace_d);
   cudaStream_t s = (cudaStream_t)stream;
   switch (cache->dtype) {
-    case TQ_F16: return attn_launch_t<tq::KV_F16>(p, cols, sms, s);
-    case TQ_BF16: return attn_launch_t<tq::KV_BF16>(p, cols, sms, s);
-    default: return attn_launch_t<tq::KV_E4M3>(p, cols, sms, s);
+    case TQ_F16: return attn_launch_t<tq::KV_F16>(p, cache, cols, sms, s);
+    case TQ_BF16: return attn_launch_t<tq::KV_BF16>(p, cache, cols, sms, s);
+    default: return attn_launch_t<tq::KV_E4M3>(p, cache, cols, sms, s);
   }
 }
 
