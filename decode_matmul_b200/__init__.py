@@ -389,6 +389,13 @@ def tq_ldlq_encode(w_rot, u, codebook, gain: float, refits: int = 1, codes=None,
 
 # ---- attention between the phases, adapters beside a projection --------------------
 
+def _raw_stream(index: int) -> int:
+    """cudaStream_t of the device's current stream (torch.cuda.current_stream without its Stream object, which costs
+    a small call as much as its launch: 3.2 against 0.1 us)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -527,7 +534,7 @@ def tq_kv_append(cache: KvCache, qkv, q_heads: int, pos, freq=None, interleaved:
         ws = _workspace_ptr(ws, 65536, dev)
         st = _lib().tq_kv_append(cache._ref, qkv.data_ptr(), width if m == 1 else qkv.stride(0), m, q_heads, _addr(seq),
                                  pos.data_ptr(), _addr(freq), 2 * half, 1 if interleaved else 0, q_out.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+                                 ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
     _ok(st, "tq_kv_append")
     return q_out
 
@@ -562,7 +569,7 @@ def tq_attn(cache: KvCache, q, pos, scale: float, seq=None, window: int = 0, out
             out = torch.empty(q.shape, dtype=torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, device=dev)
         ws = _workspace_ptr(ws, 0 if ws is not None else tq_attn_workspace(cache, m, q_heads), dev)
         st = _lib().tq_attn(cache._ref, q.data_ptr(), m, q_heads, _addr(seq), pos.data_ptr(), scale, window,
-                            out.data_ptr(), out_dtype, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+                            out.data_ptr(), out_dtype, ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
     _ok(st, "tq_attn")
     return out
 
@@ -589,6 +596,6 @@ def tq_lora(lora: Lora, x, adapter, y, out=None, ws=None, stream=None):
         ws = _workspace_ptr(ws, 0 if ws is not None else tq_lora_workspace(lora, m), dev)
         st = _lib().tq_lora(lora._ref, x.data_ptr(), m, adapter.data_ptr(), y.data_ptr(), lora.n if m <= 1 else y.stride(0),
                             out.data_ptr(), lora.n if m <= 1 else out.stride(0), ws.data_ptr(), ws.numel(),
-                            torch.cuda.current_stream().cuda_stream)
+                            _raw_stream(dev.index))
     _ok(st, "tq_lora")
     return out

@@ -155,6 +155,7 @@ constexpr int kItemCost = 2;
 // 8 x 128 bytes: 268 us one by one, the same with the heads apart in memory
 // 219 us), and for two groups of query heads on one key head.
 constexpr int kTeamMax = 4;
+constexpr int kTeamUnits = 100;  // units per block from which teams are formed
 
 // Where a warp stands in the tile order (an item here is a team's items).
 struct AttnWalk {
@@ -325,8 +326,6 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   static_assert(sizeof(Ctl) <= C::CTL, "control block");
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + W * C::WARP_BYTES);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int team = p.team, items = p.c.kv_heads * p.head_groups / team;  // items: of a team
-  const int teams = W / team, my_team = warp / team, member = warp - my_team * team;
 
   pdl_wait();
   pdl_launch_dependents();
@@ -338,9 +337,17 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   int32_t u0, u1;            // units of this warp
   int32_t b0, share, rest, blocks;  // block c takes share units, one more when c < rest
   int32_t wshare, wrest;            // and so its teams
+  int team, items, teams, my_team, member;  // items: of a team
   // false: this block has nothing to do.  A call of 2^31 units (30 TB of
   // keys and values and more) is refused.
   auto split = [&](int64_t rows_total) {
+    items = p.c.kv_heads * p.head_groups;
+    // teams leave more parts to join: not worth it for blocks with little work
+    team = rows_total * items >= (int64_t)gridDim.x * kTeamUnits ? p.team : 1;
+    items /= team;
+    teams = W / team;
+    my_team = warp / team;
+    member = warp - my_team * team;
     if (rows_total > 0x7fffffffll / items) {
       if (tid == 0 && blockIdx.x == 0) flag_bad_index(p.status);
       return false;
