@@ -1,9 +1,31 @@
 // tq_lora.cuh -- low-rank adapters of many requests beside a shared projection.
+//
+//   out[t] = y[t] + s_a B_a (A_a x_t),   a = the token's adapter
+//
+// Bound: memory.  The adapters that are used, x and y are read once and out is
+// written once; the products are a few per cent of the tensor rate.
+// Tokens of one adapter are worked on together, up to 32 in a tile (stable
+// order), by one cluster of eight blocks:
+//   1. h = A x: the cluster's warps split k (and the 16-row tiles of A); each
+//      reads its pieces of A and x straight into MMA fragments (16-byte loads;
+//      the order of k inside an MMA is permuted alike for both),
+//   2. the blocks' sums of h are exchanged through distributed shared memory,
+//      so no second launch and no trip through global memory is needed,
+//   3. each block takes an eighth of the n output features: B as the 16-row
+//      operand, tokens as the 8-wide one, 32 features in an order that gives a
+//      thread four neighbours (16-byte accesses of y and out).
+// A x keeps binary32 accuracy through the second product: it enters as three
+// bf16 terms (24 bits), or as two fp16 terms of a token's h scaled by a power
+// of two (22 bits of its largest element).
 #pragma once
 
-#include "tq_kv.cuh"
+#include <cooperative_groups.h>
+
+#include "tq_attn.cuh"
 
 namespace tq {
+
+namespace cg = cooperative_groups;
 
 struct LoraParams {
   const void* a;       // [n_adapters][rank][k]
@@ -11,58 +33,425 @@ struct LoraParams {
   const float* scale;  // [n_adapters] or null
   const void* x;       // [m][k]
   const int32_t* adapter;  // [m]
-  const float* y;      // [m][y_stride]
-  float* out;          // [m][out_stride]
+  const float* y;      // rows of y_stride
+  float* out;          // rows of out_stride
   int64_t y_stride, out_stride;
   int32_t n_adapters, rank, n, k, m;
-  float* h;  // workspace: [m][rank]
+  int32_t* plan;  // workspace (m > kLoraInBlock): tiles, perm [4096], first [4097]
   int32_t* status;
 };
 
-template <bool BF16>
-__device__ __forceinline__ float ld16(const void* p, int64_t i) {
-  if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+constexpr int LORA_THREADS = 256;
+constexpr int LORA_CLUSTER = 8;
+constexpr int kLoraTile = 32;      // tokens of a tile
+constexpr int kLoraInBlock = 256;  // up to this many tokens each block groups them for itself
+constexpr int kLoraMaxM = 4096;
+constexpr int kPlanPerm = 4, kPlanFirst = kPlanPerm + kLoraMaxM, kPlanInts = kPlanFirst + kLoraMaxM + 4;
+
+__device__ __forceinline__ int32_t lora_adapter(const LoraParams& p, int t, bool& bad) {
+  const int32_t a = p.adapter[t];
+  bad = a >= p.n_adapters;
+  return a < 0 || bad ? -1 : a;
 }
 
-// h = A x: one block per token, one warp per rank at a time.
-template <bool BF16>
-__global__ void __launch_bounds__(256) lora_shrink_kernel(LoraParams p) {
+// Grouping of more than kLoraInBlock tokens: one block sorts (adapter, token)
+// pairs in shared memory (bitonic: a fixed network, so the order is always
+// the same) and lists where each tile begins in the sorted order.
+__global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__ LoraParams p) {
+  __shared__ uint64_t key[kLoraMaxM];
+  __shared__ int32_t warp_sum[32], warp_max[32];
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x, lane = threadIdx.x & 31;
-  const int32_t ad = p.adapter[t];
-  if (ad < 0) return;
-  if (ad >= p.n_adapters) {
-    if (threadIdx.x == 0) flag_bad_index(p.status);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int size = 512;
+  while (size < p.m) size <<= 1;
+  for (int t = tid; t < size; t += 1024) {
+    uint64_t v = ~0ull;
+    if (t < p.m) {
+      bool bad;
+      const int32_t a = lora_adapter(p, t, bad);
+      if (bad) flag_bad_index(p.status);
+      v = ((uint64_t)(uint32_t)(a + 1) << 32) | (uint32_t)t;
+    }
+    key[t] = v;
+  }
+  __syncthreads();
+  for (int span = 2; span <= size; span <<= 1)
+    for (int d = span >> 1; d > 0; d >>= 1) {
+      for (int i = tid; i < size / 2; i += 1024) {
+        const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
+        const uint64_t a = key[lo], b = key[hi];
+        if ((a > b) == ((lo & span) == 0)) {
+          key[lo] = b;
+          key[hi] = a;
+        }
+      }
+      __syncthreads();
+    }
+  // a thread has four neighbours; a group's tiles begin every kLoraTile tokens of it
+  const int i0 = tid * 4;
+  int32_t start[4];  // where the token's group begins
+  int32_t run = -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i0 + i;
+    if (at < p.m && (at == 0 || (uint32_t)(key[at] >> 32) != (uint32_t)(key[at - 1] >> 32))) run = at;
+    start[i] = run;
+  }
+  int32_t before = run;  // inclusive running maximum over threads
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before = max(before, v);
+  }
+  if (lane == 31) warp_max[warp] = before;
+  __syncthreads();
+  int32_t prev = __shfl_up_sync(0xffffffffu, before, 1);
+  if (lane == 0) prev = -1;
+  for (int w = 0; w < warp; ++w) prev = max(prev, warp_max[w]);
+  int32_t lead = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    start[i] = max(start[i], prev);
+    const int at = i0 + i;
+    if (at < p.m) {
+      p.plan[kPlanPerm + at] = (int32_t)(uint32_t)key[at];
+      if ((at - start[i]) % kLoraTile == 0) ++lead;
+    }
+  }
+  int32_t incl = lead;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int32_t v = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int32_t at_tile = incl - lead, total = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) at_tile += warp_sum[w];
+    total += warp_sum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i0 + i;
+    if (at < p.m && (at - start[i]) % kLoraTile == 0) p.plan[kPlanFirst + at_tile++] = at;
+  }
+  if (tid == 0) {
+    p.plan[0] = total;
+    p.plan[kPlanFirst + total] = p.m;
+  }
+}
+
+__device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// Step 1 for NT columns of 8 tokens: this warp's sum over its k pieces.
+template <bool BF16, int NT>
+__device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int rt, const int32_t* tok, int cnt, int g0,
+                                            int g1, float* hp) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int r0 = rt * 16 + g, r1 = r0 + 8;
+  const uint16_t* a0 = static_cast<const uint16_t*>(p.a) + ((int64_t)ad * p.rank + r0) * p.k + q * 8;
+  const uint16_t* a1 = a0 + (r1 < p.rank ? (int64_t)8 * p.k : 0);
+  const bool two = r1 < p.rank;
+  const uint16_t* xp[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int c = nt * 8 + g;
+    xp[nt] = static_cast<const uint16_t*>(p.x) + (int64_t)tok[c < cnt ? c : 0] * p.k + q * 8;
+  }
+  float acc[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+  constexpr int U = NT == 4 ? 2 : 4;  // pieces of 32 features in flight together
+  for (int gi = g0; gi < g1; gi += U) {
+    uint4 a[U][2], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t o = (int64_t)(gi + u < g1 ? gi + u : g1 - 1) * 32;
+      a[u][0] = ldg16(a0 + o);
+      a[u][1] = ldg16(a1 + o);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[u][nt] = ldg16(xp[nt] + o);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (gi + u >= g1) break;
+      if (!two) a[u][1] = make_uint4(0, 0, 0, 0);
+      const uint32_t f0[4] = {a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y};
+      const uint32_t f1[4] = {a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma16<BF16>(acc[nt], f0, x[u][nt].x, x[u][nt].y);
+        mma16<BF16>(acc[nt], f1, x[u][nt].z, x[u][nt].w);
+      }
+    }
+  }
+  // [rank in tile][token]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    *reinterpret_cast<float2*>(hp + g * kLoraTile + nt * 8 + q * 2) = make_float2(acc[nt][0], acc[nt][1]);
+    *reinterpret_cast<float2*>(hp + (g + 8) * kLoraTile + nt * 8 + q * 2) = make_float2(acc[nt][2], acc[nt][3]);
+  }
+}
+
+// Step 3 for one group of 32 features and NT columns of 8 tokens.
+template <bool BF16, bool VEC, int NT>
+__device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int f0, const int32_t* tok, int cnt,
+                                            const uint16_t* planes, int pstride, const float* mul) {
+  constexpr int TERMS = BF16 ? 3 : 2;
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
+  const int f = f0 + 4 * g;
+  float4 yv[NT][2];
+  int32_t t[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = nt * 8 + q * 2 + i;
+      t[nt][i] = c < cnt ? tok[c] : -1;
+      yv[nt][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t[nt][i] >= 0 && f < p.n) {
+        const float* src = p.y + t[nt][i] * p.y_stride + f;
+        if (VEC && f + 4 <= p.n) {
+          yv[nt][i] = *reinterpret_cast<const float4*>(src);
+        } else {
+          yv[nt][i].x = src[0];
+          if (f + 1 < p.n) yv[nt][i].y = src[1];
+          if (f + 2 < p.n) yv[nt][i].z = src[2];
+          if (f + 3 < p.n) yv[nt][i].w = src[3];
+        }
+      }
+    }
+  float acc[2][NT][4];
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
+  const uint16_t* bp = static_cast<const uint16_t*>(p.b) + ((int64_t)ad * p.n + f) * p.rank + q * 4;
+#pragma unroll 2
+  for (int r = 0; r < p.rank; r += 16) {
+    const bool in = r + q * 4 < p.rank;  // the last 8 of an odd number of eights
+    uint2 b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      b[i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + (int64_t)i * p.rank + r)) : make_uint2(0, 0);
+    const uint32_t m0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, m1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
+#pragma unroll
+    for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
+        mma16<BF16>(acc[0][nt], m0, h.x, h.y);
+        mma16<BF16>(acc[1][nt], m1, h.x, h.y);
+      }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (t[nt][i] < 0 || f >= p.n) continue;
+      const float s = mul[nt * 8 + q * 2 + i];
+      float4 v = yv[nt][i];
+      v.x = fmaf(acc[0][nt][i], s, v.x);
+      v.y = fmaf(acc[0][nt][2 + i], s, v.y);
+      v.z = fmaf(acc[1][nt][i], s, v.z);
+      v.w = fmaf(acc[1][nt][2 + i], s, v.w);
+      float* dst = p.out + t[nt][i] * p.out_stride + f;
+      if (VEC && f + 4 <= p.n) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {
+        dst[0] = v.x;
+        if (f + 1 < p.n) dst[1] = v.y;
+        if (f + 2 < p.n) dst[2] = v.z;
+        if (f + 3 < p.n) dst[3] = v.w;
+      }
+    }
+}
+
+template <bool BF16, bool VEC>
+__global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS)
+    lora_kernel(const __grid_constant__ LoraParams p) {
+  constexpr int WARPS = LORA_THREADS / 32;
+  constexpr int PLANE_STRIDE = 128 + 16;  // the row of one token (8 words past a multiple of 32: no bank conflicts)
+  __shared__ int32_t ids[kLoraInBlock + 4], tok[kLoraTile], head[4], lead_count[WARPS];
+  __shared__ float mul[kLoraTile];
+  __shared__ __align__(16) float h[128 * kLoraTile];  // the block's sum of A x: [rank][token]
+  // the warps' sums, and later the terms of h: [term][token][rank]
+  constexpr int PLANE_BYTES = 3 * kLoraTile * PLANE_STRIDE * 2, HP_BYTES = WARPS * 16 * kLoraTile * 4;
+  __shared__ __align__(16) uint8_t scratch[PLANE_BYTES > HP_BYTES ? PLANE_BYTES : HP_BYTES];
+  float* hp = reinterpret_cast<float*>(scratch);
+  uint16_t* planes = reinterpret_cast<uint16_t*>(scratch);
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int part = cluster.block_rank();
+  const int tile = blockIdx.x / LORA_CLUSTER;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- the tile's tokens -------------------------------------------------------
+  int cnt;
+  int32_t ad;
+  if (p.m > kLoraInBlock) {
+    if (tile >= p.plan[0]) return;  // the whole cluster
+    const int i0 = p.plan[kPlanFirst + tile];
+    cnt = p.plan[kPlanFirst + tile + 1] - i0;
+    if (tid < cnt) tok[tid] = p.plan[kPlanPerm + i0 + tid];
+    bool bad;
+    ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
+    __syncthreads();
+  } else {
+    int32_t id = -1;
+    if (tid < p.m) {
+      bool bad;
+      id = lora_adapter(p, tid, bad);
+      if (bad && blockIdx.x == 0) flag_bad_index(p.status);
+    }
+    ids[tid] = id;
+    if (tid == 0) head[0] = -1;
+    __syncthreads();
+    // how many tokens of the same adapter come before this one
+    int before = 0;
+    if (tid < p.m) {
+      const int4* v = reinterpret_cast<const int4*>(ids);
+      for (int s = 0; s < tid; s += 4) {
+        const int4 o = v[s >> 2];
+        before += (o.x == id) + (s + 1 < tid && o.y == id) + (s + 2 < tid && o.z == id) + (s + 3 < tid && o.w == id);
+      }
+    }
+    const bool lead = tid < p.m && before % kLoraTile == 0;
+    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+    if (lane == 0) lead_count[warp] = __popc(leads);
+    __syncthreads();
+    int mine = __popc(leads & ((1u << lane) - 1)), total = 0;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) mine += lead_count[w];
+      total += lead_count[w];
+    }
+    if (tile >= total) return;  // the whole cluster
+    if (lead && mine == tile) {
+      head[0] = id;
+      head[1] = before;
+      head[2] = 0;
+    }
+    __syncthreads();
+    ad = head[0];
+    const int first = head[1];
+    const bool in = tid < p.m && id == ad && before >= first && before < first + kLoraTile;
+    if (in) tok[before - first] = tid;
+    cnt = __syncthreads_count(in);
+  }
+
+  if (ad < 0) {  // no adapter: y as it is
+    if (p.out != p.y)
+      for (int c = 0; c < cnt; ++c) {
+        const float* src = p.y + tok[c] * p.y_stride;
+        float* dst = p.out + tok[c] * p.out_stride;
+        if (VEC) {
+          const int quads = p.n >> 2;
+          for (int i = part * LORA_THREADS + tid; i < quads; i += LORA_CLUSTER * LORA_THREADS)
+            reinterpret_cast<float4*>(dst)[i] = reinterpret_cast<const float4*>(src)[i];
+          for (int i = quads * 4 + part * LORA_THREADS + tid; i < p.n; i += LORA_CLUSTER * LORA_THREADS) dst[i] = src[i];
+        } else {
+          for (int i = part * LORA_THREADS + tid; i < p.n; i += LORA_CLUSTER * LORA_THREADS) dst[i] = src[i];
+        }
+      }
     return;
   }
-  for (int r = threadIdx.x >> 5; r < p.rank; r += 8) {
-    const int64_t arow = ((int64_t)ad * p.rank + r) * p.k;
-    float s = 0.f;
-    for (int i = lane; i < p.k; i += 32) s += ld16<BF16>(p.a, arow + i) * ld16<BF16>(p.x, (int64_t)t * p.k + i);
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    if (lane == 0) p.h[(int64_t)t * p.rank + r] = s;
-  }
-}
 
-// y' = y + s B h: a thread per output feature.
-template <bool BF16>
-__global__ void __launch_bounds__(256) lora_expand_kernel(LoraParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int t = blockIdx.x;
-  const int n = blockIdx.y * 256 + threadIdx.x;
-  if (n >= p.n) return;
-  const int32_t ad = p.adapter[t];
-  float v = p.y[(int64_t)t * p.y_stride + n];
-  if (ad >= 0 && ad < p.n_adapters) {
-    float s = 0.f;
-    for (int r = 0; r < p.rank; ++r)
-      s += ld16<BF16>(p.b, ((int64_t)ad * p.n + n) * p.rank + r) * p.h[(int64_t)t * p.rank + r];
-    v += (p.scale ? p.scale[ad] : 1.f) * s;
+  // ---- 1. h = A x over this block's share of k -----------------------------------
+  const int rts = (p.rank + 15) >> 4;         // 16-row tiles of A
+  const int kparts = WARPS / rts;             // warps that share a tile's k
+  const int rt = warp / kparts, kp = warp - rt * kparts;
+  if (rt < rts) {
+    const int pieces = p.k >> 5, shares = LORA_CLUSTER * kparts, s = part * kparts + kp;
+    const int g0 = (int)((int64_t)pieces * s / shares), g1 = (int)((int64_t)pieces * (s + 1) / shares);
+    float* to = hp + warp * 16 * kLoraTile;
+    if (cnt <= 8)
+      lora_shrink<BF16, 1>(p, ad, rt, tok, cnt, g0, g1, to);
+    else if (cnt <= 16)
+      lora_shrink<BF16, 2>(p, ad, rt, tok, cnt, g0, g1, to);
+    else
+      lora_shrink<BF16, 4>(p, ad, rt, tok, cnt, g0, g1, to);
   }
-  p.out[(int64_t)t * p.out_stride + n] = v;
+  __syncthreads();
+  const int cols = cnt <= 8 ? 8 : (cnt <= 16 ? 16 : 32), cshift = cnt <= 8 ? 3 : (cnt <= 16 ? 4 : 5);
+  for (int i = tid; i < p.rank << cshift; i += LORA_THREADS) {
+    const int r = i >> cshift, c = i & (cols - 1);
+    const float* src = hp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * kLoraTile + c;
+    float s = 0.f;
+    for (int w = 0; w < kparts; ++w) s += src[w * 16 * kLoraTile];
+    h[r * kLoraTile + c] = s;
+  }
+  cluster.sync();
+
+  // ---- 2. the cluster's sum, as terms of the operand type --------------------------
+  // one warp per token: lane l has ranks l, l + 32, ...
+  const float sa = p.scale ? p.scale[ad] : 1.f;
+  const int ranks = rts * 16;  // the last tile's missing ranks are zero terms
+  for (int c = warp; c < cols; c += WARPS) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = j * 32 + lane;
+      if (r < p.rank && c < cnt) {
+        float part_h[LORA_CLUSTER];
+#pragma unroll
+        for (int b = 0; b < LORA_CLUSTER; ++b) part_h[b] = cluster.map_shared_rank(h, b)[r * kLoraTile + c];
+#pragma unroll
+        for (int b = 0; b < LORA_CLUSTER; ++b) v[j] += part_h[b];
+      }
+    }
+    float up = 1.f;  // what the scaled terms are multiplied by
+    if constexpr (!BF16) {
+      float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      // the largest element goes to [2^9, 2^10)
+      const int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;
+      if (e > -110 && e < 120) {
+        up = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+        const float down = __uint_as_float((uint32_t)(9 - e + 127) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= down;
+      }
+    }
+    if (lane == 0) mul[c] = sa * up;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = j * 32 + lane;
+      if (r >= ranks) continue;
+      float rest = v[j];
+#pragma unroll
+      for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
+        const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
+        planes[(term * kLoraTile + c) * PLANE_STRIDE + r] = t;
+        const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
+        rest = fabsf(back) < INFINITY ? rest - back : 0.f;
+      }
+    }
+  }
+  __syncthreads();
+
+  // ---- 3. out = y + s B h over this block's share of n -------------------------------
+  const int groups = (p.n + 31) >> 5;
+  const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER), e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
+  for (int e = e0 + warp; e < e1; e += WARPS) {
+    if (cnt <= 8)
+      lora_expand<BF16, VEC, 1>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
+    else if (cnt <= 16)
+      lora_expand<BF16, VEC, 2>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
+    else
+      lora_expand<BF16, VEC, 4>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
+  }
+  cluster.sync();  // the other blocks have read this one's h
 }
 
 }  // namespace tq

@@ -164,7 +164,9 @@ int check_lora(const tq_lora_t* l) {
   return TQ_OK;
 }
 
-size_t lora_ws_bytes(const tq_lora_t* l, int32_t m) { return kCounterBytes + (size_t)m * l->rank * sizeof(float); }
+size_t lora_ws_bytes(int32_t m) {
+  return kCounterBytes + (m > tq::kLoraInBlock ? (size_t)tq::kPlanInts * sizeof(int32_t) : 0);
+}
 
 }  // namespace
 
@@ -280,7 +282,7 @@ int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes) {
   int st = check_lora(lora);
   if (st != TQ_OK) return st;
   if (m < 0 || m > kMaxM) return TQ_ERR_SHAPE;
-  *bytes = lora_ws_bytes(lora, m);
+  *bytes = lora_ws_bytes(m);
   return TQ_OK;
 }
 
@@ -292,7 +294,7 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   if (m == 0) return TQ_OK;
   if (!x_d || !adapter_d || !y_d || !out_d) return TQ_ERR_NULL;
   if (!aligned16(x_d) || !aligned_to(adapter_d, 4) || !aligned_to(y_d, 4) || !aligned_to(out_d, 4)) return TQ_ERR_ALIGN;
-  st = check_ws(workspace_d, ws_bytes, lora_ws_bytes(lora, m));
+  st = check_ws(workspace_d, ws_bytes, lora_ws_bytes(m));
   if (st != TQ_OK) return st;
   int sms = 0;
   st = check_arch(&sms);
@@ -312,16 +314,23 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   p.n = lora->n;
   p.k = lora->k;
   p.m = m;
-  p.h = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + kCounterBytes);
+  p.plan = reinterpret_cast<int32_t*>(static_cast<char*>(workspace_d) + kCounterBytes);
   p.status = status_word(workspace_d);
   cudaStream_t s = (cudaStream_t)stream;
-  const bool bf = lora->dtype == TQ_BF16;
-  st = bf ? launch(tq::lora_shrink_kernel<true>, dim3((unsigned)m), dim3(256), 0, s, p)
-          : launch(tq::lora_shrink_kernel<false>, dim3((unsigned)m), dim3(256), 0, s, p);
-  if (st != TQ_OK) return st;
-  const dim3 grid((unsigned)m, (unsigned)((lora->n + 255) / 256));
-  return bf ? launch(tq::lora_expand_kernel<true>, grid, dim3(256), 0, s, p)
-            : launch(tq::lora_expand_kernel<false>, grid, dim3(256), 0, s, p);
+  if (m > tq::kLoraInBlock) {
+    st = launch(tq::lora_plan_kernel, dim3(1), dim3(1024), 0, s, p);
+    if (st != TQ_OK) return st;
+  }
+  // tiles: every adapter (and the tokens without one) adds at most one that is not full
+  int64_t tiles = (int64_t)(m / tq::kLoraTile) + lora->n_adapters + 1;
+  if (tiles > m) tiles = m;
+  const dim3 grid((unsigned)tiles * tq::LORA_CLUSTER), block(tq::LORA_THREADS);
+  const bool vec = aligned16(y_d) && aligned16(out_d) && y_stride % 4 == 0 && out_stride % 4 == 0;
+  if (lora->dtype == TQ_BF16)
+    return vec ? launch(tq::lora_kernel<true, true>, grid, block, 0, s, p)
+               : launch(tq::lora_kernel<true, false>, grid, block, 0, s, p);
+  return vec ? launch(tq::lora_kernel<false, true>, grid, block, 0, s, p)
+             : launch(tq::lora_kernel<false, false>, grid, block, 0, s, p);
 }
 
 }  // extern "C"

@@ -102,7 +102,7 @@ def test_lora_checks():
                      (dict(os=999), tq.TQ_ERR_SHAPE), (dict(x=None), tq.TQ_ERR_NULL), (dict(ad=None), tq.TQ_ERR_NULL),
                      (dict(y=None), tq.TQ_ERR_NULL), (dict(out=None), tq.TQ_ERR_NULL), (dict(x=24), tq.TQ_ERR_ALIGN),
                      (dict(y=18), tq.TQ_ERR_ALIGN), (dict(ad=18), tq.TQ_ERR_ALIGN), (dict(ws=None), tq.TQ_ERR_WORKSPACE),
-                     (dict(n=65536), tq.TQ_ERR_WORKSPACE), (dict(m=0, x=None), tq.TQ_OK)]:
+                     (dict(n=65535), tq.TQ_ERR_WORKSPACE), (dict(m=0, x=None), tq.TQ_OK)]:
         assert call(None, **kw) == want, kw
 
 
