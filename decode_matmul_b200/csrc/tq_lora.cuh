@@ -54,40 +54,74 @@ __device__ __forceinline__ int32_t lora_adapter(const LoraParams& p, int t, bool
   return a < 0 || bad ? -1 : a;
 }
 
-// Grouping of more than kLoraInBlock tokens: one block sorts (adapter, token)
-// pairs in shared memory (bitonic: a fixed network, so the order is always
-// the same) and lists where each tile begins in the sorted order.
+// Grouping of more than kLoraInBlock tokens, by one block: a stable radix sort
+// of (adapter, token) in shared memory, five bits a pass (40 adapters: two
+// passes), then a list of where each tile begins in the sorted order.  A warp
+// takes 128 tokens in their order, 32 at a time; lanes with the same digit find
+// one another by a match, so no atomics are needed and the order is always the
+// same.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__ LoraParams p) {
-  __shared__ uint64_t key[kLoraMaxM];
+  __shared__ uint32_t key[2][kLoraMaxM];  // (adapter + 1) << 12 | token
+  __shared__ int32_t count[32][33];  // [digit][warp]
   __shared__ int32_t warp_sum[32], warp_max[32];
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int size = 512;
-  while (size < p.m) size <<= 1;
-  for (int t = tid; t < size; t += 1024) {
-    uint64_t v = ~0ull;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = i * 1024 + tid;
+    uint32_t v = 0xffffffffu;  // behind the last token
     if (t < p.m) {
       bool bad;
-      const int32_t a = lora_adapter(p, t, bad);
+      v = (uint32_t)(lora_adapter(p, t, bad) + 1) << 12 | (uint32_t)t;
       if (bad) flag_bad_index(p.status);
-      v = ((uint64_t)(uint32_t)(a + 1) << 32) | (uint32_t)t;
     }
-    key[t] = v;
+    key[0][t] = v;
   }
-  __syncthreads();
-  for (int span = 2; span <= size; span <<= 1)
-    for (int d = span >> 1; d > 0; d >>= 1) {
-      for (int i = tid; i < size / 2; i += 1024) {
-        const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-        const uint64_t a = key[lo], b = key[hi];
-        if ((a > b) == ((lo & span) == 0)) {
-          key[lo] = b;
-          key[hi] = a;
-        }
-      }
-      __syncthreads();
+  int cur = 0;
+  const int bits = 32 - __clz(p.n_adapters + 1);  // so that the padding's bits are above all adapters'
+  for (int shift = 12; shift < 12 + bits; shift += 5) {
+    count[lane][warp] = 0;
+    __syncthreads();
+    uint32_t v[4];
+    int32_t rank[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = warp * 128 + i * 32 + lane;
+      v[i] = key[cur][at];
+      const int digit = (v[i] >> shift) & 31;
+      const uint32_t same = __match_any_sync(0xffffffffu, digit);
+      const int first = __ffs(same) - 1;
+      const int base = count[digit][warp];
+      __syncwarp();
+      if (lane == first) count[digit][warp] = base + __popc(same);
+      __syncwarp();
+      rank[i] = base + __popc(same & ((1u << lane) - 1));
     }
+    __syncthreads();
+    // exclusive sums over (digit, warp) in that order: thread (d = warp, w = lane)
+    const int32_t c = count[warp][lane];
+    int32_t incl = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += u;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int32_t prior = lane < warp ? warp_sum[lane] : 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) prior += __shfl_xor_sync(0xffffffffu, prior, d);
+    count[warp][lane] = prior + incl - c;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int to = count[(v[i] >> shift) & 31][warp] + rank[i];
+      key[cur ^ 1][to] = v[i];
+    }
+    cur ^= 1;
+    __syncthreads();
+  }
   // a thread has four neighbours; a group's tiles begin every kLoraTile tokens of it
   const int i0 = tid * 4;
   int32_t start[4];  // where the token's group begins
@@ -95,7 +129,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i0 + i;
-    if (at < p.m && (at == 0 || (uint32_t)(key[at] >> 32) != (uint32_t)(key[at - 1] >> 32))) run = at;
+    if (at < p.m && (at == 0 || (key[cur][at] >> 12) != (key[cur][at - 1] >> 12))) run = at;
     start[i] = run;
   }
   int32_t before = run;  // inclusive running maximum over threads
@@ -115,7 +149,7 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
     start[i] = max(start[i], prev);
     const int at = i0 + i;
     if (at < p.m) {
-      p.plan[kPlanPerm + at] = (int32_t)(uint32_t)key[at];
+      p.plan[kPlanPerm + at] = (int32_t)(key[cur][at] & 4095u);
       if ((at - start[i]) % kLoraTile == 0) ++lead;
     }
   }
@@ -197,25 +231,38 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   }
 }
 
-// Step 3 for one group of 32 features and NT columns of 8 tokens.
+// Step 3 for one group of 32 features and NT columns of 8 tokens.  All of its
+// loads (y, and B up to rank 64) are issued before the first is used.
 template <bool BF16, bool VEC, int NT>
 __device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int f0, const int32_t* tok, int cnt,
                                             const uint16_t* planes, int pstride, const float* mul) {
   constexpr int TERMS = BF16 ? 3 : 2;
+  constexpr int AHEAD = 4;  // steps of 16 ranks loaded together
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
   const int f = f0 + 4 * g;
+  const uint16_t* bp = static_cast<const uint16_t*>(p.b) + ((int64_t)ad * p.n + f) * p.rank + q * 4;
+  uint2 b[AHEAD][4];
+  auto load_b = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int r = r0 + u * 16;
+      const bool in = r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[u][i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + i * p.rank + r)) : make_uint2(0, 0);
+    }
+  };
+  load_b(0);
   float4 yv[NT][2];
-  int32_t t[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int c = nt * 8 + q * 2 + i;
-      t[nt][i] = c < cnt ? tok[c] : -1;
       yv[nt][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t[nt][i] >= 0 && f < p.n) {
-        const float* src = p.y + t[nt][i] * p.y_stride + f;
+      if (c < cnt && f < p.n) {
+        const float* src = p.y + tok[c] * p.y_stride + f;
         if (VEC && f + 4 <= p.n) {
           yv[nt][i] = *reinterpret_cast<const float4*>(src);
         } else {
@@ -233,36 +280,37 @@ __device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
-  const uint16_t* bp = static_cast<const uint16_t*>(p.b) + ((int64_t)ad * p.n + f) * p.rank + q * 4;
-#pragma unroll 2
-  for (int r = 0; r < p.rank; r += 16) {
-    const bool in = r + q * 4 < p.rank;  // the last 8 of an odd number of eights
-    uint2 b[4];
+  for (int r0 = 0; r0 < p.rank; r0 += 16 * AHEAD) {
+    if (r0 > 0) load_b(r0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      b[i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + (int64_t)i * p.rank + r)) : make_uint2(0, 0);
-    const uint32_t m0[4] = {b[0].x, b[1].x, b[0].y, b[1].y}, m1[4] = {b[2].x, b[3].x, b[2].y, b[3].y};
+    for (int u = 0; u < AHEAD; ++u) {
+      const int r = r0 + u * 16;
+      if (r >= p.rank) break;
+      const uint32_t m0[4] = {b[u][0].x, b[u][1].x, b[u][0].y, b[u][1].y};
+      const uint32_t m1[4] = {b[u][2].x, b[u][3].x, b[u][2].y, b[u][3].y};
 #pragma unroll
-    for (int term = 0; term < TERMS; ++term)
+      for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
-        mma16<BF16>(acc[0][nt], m0, h.x, h.y);
-        mma16<BF16>(acc[1][nt], m1, h.x, h.y);
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
+          mma16<BF16>(acc[0][nt], m0, h.x, h.y);
+          mma16<BF16>(acc[1][nt], m1, h.x, h.y);
+        }
+    }
   }
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (t[nt][i] < 0 || f >= p.n) continue;
-      const float s = mul[nt * 8 + q * 2 + i];
+      const int c = nt * 8 + q * 2 + i;
+      if (c >= cnt || f >= p.n) continue;
+      const float s = mul[c];
       float4 v = yv[nt][i];
       v.x = fmaf(acc[0][nt][i], s, v.x);
       v.y = fmaf(acc[0][nt][2 + i], s, v.y);
       v.z = fmaf(acc[1][nt][i], s, v.z);
       v.w = fmaf(acc[1][nt][2 + i], s, v.w);
-      float* dst = p.out + t[nt][i] * p.out_stride + f;
+      float* dst = p.out + tok[c] * p.out_stride + f;
       if (VEC && f + 4 <= p.n) {
         *reinterpret_cast<float4*>(dst) = v;
       } else {
@@ -275,7 +323,7 @@ __device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int
 }
 
 template <bool BF16, bool VEC>
-__global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS)
+__global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 2)
     lora_kernel(const __grid_constant__ LoraParams p) {
   constexpr int WARPS = LORA_THREADS / 32;
   constexpr int PLANE_STRIDE = 128 + 16;  // the row of one token (8 words past a multiple of 32: no bank conflicts)

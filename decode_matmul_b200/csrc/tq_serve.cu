@@ -157,7 +157,7 @@ int attn_launch_t(const tq::AttnParams& p, const tq_kv_cache_t* c, int cols, int
 int check_lora(const tq_lora_t* l) {
   if (!l) return TQ_ERR_NULL;
   if (l->dtype != TQ_F16 && l->dtype != TQ_BF16) return TQ_ERR_VALUE;
-  if (l->n_adapters < 1 || l->n < 1 || l->k < 512 || l->k % 512 != 0) return TQ_ERR_SHAPE;
+  if (l->n_adapters < 1 || l->n_adapters > TQ_LORA_MAX_ADAPTERS || l->n < 1 || l->k < 512 || l->k % 512 != 0) return TQ_ERR_SHAPE;
   if (l->rank < 8 || l->rank > TQ_LORA_MAX_RANK || l->rank % 8 != 0) return TQ_ERR_SHAPE;
   if (!l->a_d || !l->b_d) return TQ_ERR_NULL;
   if (!aligned16(l->a_d) || !aligned16(l->b_d) || !aligned_to(l->scale_d, 4)) return TQ_ERR_ALIGN;

@@ -470,8 +470,10 @@ TQ_API int tq_attn(const tq_kv_cache_t* cache, const void* q_d, int32_t m, int32
  *   dtype TQ_BF16 or TQ_F16, 16-byte aligned.  scale_d: device fp32
  *   [n_adapters], or NULL = 1.
  * rank: a multiple of 8, 8 .. TQ_LORA_MAX_RANK (pad smaller adapters with
- *   zeros).  k: a positive multiple of 512.  n >= 1. */
+ *   zeros).  k: a positive multiple of 512.  n >= 1.
+ * n_adapters: 1 .. TQ_LORA_MAX_ADAPTERS. */
 #define TQ_LORA_MAX_RANK 128
+#define TQ_LORA_MAX_ADAPTERS 1000000
 typedef struct tq_lora {
   const void* a_d;
   const void* b_d;
