@@ -199,7 +199,7 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
-  constexpr int U = NT == 4 ? 2 : 4;  // pieces of 32 features in flight together
+  constexpr int U = NT == 4 ? 3 : (NT == 2 ? 4 : 8);  // pieces of 32 features in flight together
   for (int gi = g0; gi < g1; gi += U) {
     uint4 a[U][2], x[U][NT];
 #pragma unroll
@@ -231,110 +231,185 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   }
 }
 
-// Step 3 for one group of 32 features and NT columns of 8 tokens.  All of its
-// loads (y, and B up to rank 64) are issued before the first is used.
-template <bool BF16, bool VEC, int NT>
-__device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int f0, const int32_t* tok, int cnt,
-                                            const uint16_t* planes, int pstride, const float* mul) {
+// Step 3 for NT columns of 8 tokens: this warp's groups of 32 features, e0,
+// e0 + step, ... below e1.  GN groups are worked on together; B is loaded
+// AHEAD steps of 16 ranks at a time, before the steps in hand are multiplied.
+// RING: y comes through this warp's two buffers in shared memory, copied a
+// round ahead (with 32 tokens its registers would not leave room to have the
+// next group's loads in flight).
+template <bool BF16, bool VEC, int NT, int GN, int AHEAD, bool RING>
+__device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int e0, int e1, int step, const int32_t* tok,
+                                            int cnt, const uint16_t* planes, int pstride, const float* mul, uint8_t* ring) {
+  static_assert(!RING || (VEC && GN == 1), "ring");
   constexpr int TERMS = BF16 ? 3 : 2;
-  constexpr int AHEAD = 4;  // steps of 16 ranks loaded together
+  constexpr int STAGE = NT * 8 * 128;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
-  const int f = f0 + 4 * g;
-  const uint16_t* bp = static_cast<const uint16_t*>(p.b) + ((int64_t)ad * p.n + f) * p.rank + q * 4;
-  uint2 b[AHEAD][4];
-  auto load_b = [&](int r0) {
+  const uint16_t* bp = static_cast<const uint16_t*>(p.b) + (int64_t)ad * p.n * p.rank + q * 4;
+  const uint32_t ring_u = RING ? smem_u32(ring) : 0;
+  // row c of a stage is token c's 8 chunks of 4 features, chunk i at i ^ ((c >> 1) & 3) * 2
+  auto fetch = [&](int e, int stage) {
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int r = r0 + u * 16;
-      const bool in = r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[u][i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + i * p.rank + r)) : make_uint2(0, 0);
+    for (int i = 0; i < NT * 2; ++i) {
+      const int c = i * 4 + (lane >> 3), ch = lane & 7, f = e * 32 + ch * 4;
+      const bool in = e < e1 && c < cnt && f + 4 <= p.n;
+      const float* src = in ? p.y + tok[c] * p.y_stride + f : p.y;
+      cp_async16(ring_u + stage * STAGE + c * 128 + (ch ^ (((c >> 1) & 3) * 2)) * 16, src, in);
     }
+    cp_async_commit();
   };
-  load_b(0);
-  float4 yv[NT][2];
+  int stage = 0;
+  if (RING) fetch(e0, 0);
+  for (int e = e0; e < e1; e += GN * step) {
+    uint2 b[GN][AHEAD][4];
+    auto load_b = [&](int r0) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+      for (int j = 0; j < GN; ++j) {
+        const int f = (e + j * step) * 32 + 4 * g;
+        const bool on = e + j * step < e1;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = nt * 8 + q * 2 + i;
-      yv[nt][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c < cnt && f < p.n) {
-        const float* src = p.y + tok[c] * p.y_stride + f;
-        if (VEC && f + 4 <= p.n) {
-          yv[nt][i] = *reinterpret_cast<const float4*>(src);
-        } else {
-          yv[nt][i].x = src[0];
-          if (f + 1 < p.n) yv[nt][i].y = src[1];
-          if (f + 2 < p.n) yv[nt][i].z = src[2];
-          if (f + 3 < p.n) yv[nt][i].w = src[3];
+        for (int u = 0; u < AHEAD; ++u) {
+          const int r = r0 + u * 16;
+          const bool in = on && r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            b[j][u][i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + (int64_t)(f + i) * p.rank + r))
+                                           : make_uint2(0, 0);
         }
       }
+    };
+    load_b(0);
+    if (RING) fetch(e + step, stage ^ 1);
+    float4 yv[GN][NT][2];
+    if (!RING) {
+#pragma unroll
+      for (int j = 0; j < GN; ++j) {
+        const int f = (e + j * step) * 32 + 4 * g;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = nt * 8 + q * 2 + i;
+            float4& v = yv[j][nt][i];
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (e + j * step < e1 && c < cnt && f < p.n) {
+              const float* src = p.y + tok[c] * p.y_stride + f;
+              if (VEC && f + 4 <= p.n) {
+                v = *reinterpret_cast<const float4*>(src);
+              } else {
+                v.x = src[0];
+                if (f + 1 < p.n) v.y = src[1];
+                if (f + 2 < p.n) v.z = src[2];
+                if (f + 3 < p.n) v.w = src[3];
+              }
+            }
+          }
+      }
     }
-  float acc[2][NT][4];
+    float acc[GN][2][NT][4];
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
+    for (int j = 0; j < GN; ++j)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mt][nt][i] = 0.f;
-  for (int r0 = 0; r0 < p.rank; r0 += 16 * AHEAD) {
-    if (r0 > 0) load_b(r0);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int r = r0 + u * 16;
-      if (r >= p.rank) break;
-      const uint32_t m0[4] = {b[u][0].x, b[u][1].x, b[u][0].y, b[u][1].y};
-      const uint32_t m1[4] = {b[u][2].x, b[u][3].x, b[u][2].y, b[u][3].y};
+          for (int i = 0; i < 4; ++i) acc[j][mt][nt][i] = 0.f;
+    for (int r0 = 0; r0 < p.rank; r0 += 16 * AHEAD) {
 #pragma unroll
-      for (int term = 0; term < TERMS; ++term)
+      for (int u = 0; u < AHEAD; ++u) {
+        const int r = r0 + u * 16;
+        if (r >= p.rank) break;
+        uint32_t m0[GN][4], m1[GN][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
-          mma16<BF16>(acc[0][nt], m0, h.x, h.y);
-          mma16<BF16>(acc[1][nt], m1, h.x, h.y);
+        for (int j = 0; j < GN; ++j) {
+          m0[j][0] = b[j][u][0].x, m0[j][1] = b[j][u][1].x, m0[j][2] = b[j][u][0].y, m0[j][3] = b[j][u][1].y;
+          m1[j][0] = b[j][u][2].x, m1[j][1] = b[j][u][3].x, m1[j][2] = b[j][u][2].y, m1[j][3] = b[j][u][3].y;
+        }
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
+#pragma unroll
+            for (int j = 0; j < GN; ++j) {
+              mma16<BF16>(acc[j][0][nt], m0[j], h.x, h.y);
+              mma16<BF16>(acc[j][1][nt], m1[j], h.x, h.y);
+            }
+          }
+      }
+      if (r0 + 16 * AHEAD < p.rank) load_b(r0 + 16 * AHEAD);
+    }
+    if (RING) {
+      cp_async_wait<1>();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int j = 0; j < GN; ++j) {
+      const int f = (e + j * step) * 32 + 4 * g;
+      if (e + j * step >= e1) break;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = nt * 8 + q * 2 + i;
+          if (c >= cnt || f >= p.n) continue;
+          float4 v = yv[j][nt][i];
+          if (RING) {
+            v = *reinterpret_cast<const float4*>(ring + stage * STAGE + c * 128 + (g ^ (q * 2)) * 16);
+            if (f + 4 > p.n) {  // the last features of an odd n were not copied
+              const float* src = p.y + tok[c] * p.y_stride + f;
+              v.x = src[0];
+              if (f + 1 < p.n) v.y = src[1];
+              if (f + 2 < p.n) v.z = src[2];
+            }
+          }
+          const float s = mul[c];
+          v.x = fmaf(acc[j][0][nt][i], s, v.x);
+          v.y = fmaf(acc[j][0][nt][2 + i], s, v.y);
+          v.z = fmaf(acc[j][1][nt][i], s, v.z);
+          v.w = fmaf(acc[j][1][nt][2 + i], s, v.w);
+          float* dst = p.out + tok[c] * p.out_stride + f;
+          if (VEC && f + 4 <= p.n) {
+            *reinterpret_cast<float4*>(dst) = v;
+          } else {
+            dst[0] = v.x;
+            if (f + 1 < p.n) dst[1] = v.y;
+            if (f + 2 < p.n) dst[2] = v.z;
+            if (f + 3 < p.n) dst[3] = v.w;
+          }
         }
     }
+    stage ^= 1;
+    if (RING) __syncwarp();  // the buffer is read before it is filled again
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = nt * 8 + q * 2 + i;
-      if (c >= cnt || f >= p.n) continue;
-      const float s = mul[c];
-      float4 v = yv[nt][i];
-      v.x = fmaf(acc[0][nt][i], s, v.x);
-      v.y = fmaf(acc[0][nt][2 + i], s, v.y);
-      v.z = fmaf(acc[1][nt][i], s, v.z);
-      v.w = fmaf(acc[1][nt][2 + i], s, v.w);
-      float* dst = p.out + tok[c] * p.out_stride + f;
-      if (VEC && f + 4 <= p.n) {
-        *reinterpret_cast<float4*>(dst) = v;
-      } else {
-        dst[0] = v.x;
-        if (f + 1 < p.n) dst[1] = v.y;
-        if (f + 2 < p.n) dst[2] = v.z;
-        if (f + 3 < p.n) dst[3] = v.w;
-      }
-    }
 }
+
+// Shared memory of a block.  The copies of y (step 3) take the place of the
+// sums of A x (steps 1 and 2).
+struct LoraSmem {
+  static constexpr int PSTRIDE = 128 + 16;  // a token's terms, 8 words past a multiple of 32 (no bank conflicts)
+  static constexpr int WARPS = LORA_THREADS / 32;
+  int32_t ids[kLoraInBlock], tok[kLoraTile], head[4], lead_count[WARPS];
+  float mul[kLoraTile];
+  uint16_t planes[3 * kLoraTile * PSTRIDE];  // [term][token][rank]
+  union alignas(16) {
+    struct {
+      float h[128 * kLoraTile];      // the block's sum: [rank][token]
+      float total[128 * kLoraTile];  // the cluster's
+      float warp[WARPS * 16 * kLoraTile];
+    };
+    uint8_t ring[WARPS * 2 * kLoraTile * 128];
+  };
+};
 
 template <bool BF16, bool VEC>
 __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 2)
     lora_kernel(const __grid_constant__ LoraParams p) {
   constexpr int WARPS = LORA_THREADS / 32;
-  constexpr int PLANE_STRIDE = 128 + 16;  // the row of one token (8 words past a multiple of 32: no bank conflicts)
-  __shared__ int32_t ids[kLoraInBlock + 4], tok[kLoraTile], head[4], lead_count[WARPS];
-  __shared__ float mul[kLoraTile];
-  __shared__ __align__(16) float h[128 * kLoraTile];  // the block's sum of A x: [rank][token]
-  // the warps' sums, and later the terms of h: [term][token][rank]
-  constexpr int PLANE_BYTES = 3 * kLoraTile * PLANE_STRIDE * 2, HP_BYTES = WARPS * 16 * kLoraTile * 4;
-  __shared__ __align__(16) uint8_t scratch[PLANE_BYTES > HP_BYTES ? PLANE_BYTES : HP_BYTES];
-  float* hp = reinterpret_cast<float*>(scratch);
-  uint16_t* planes = reinterpret_cast<uint16_t*>(scratch);
+  extern __shared__ __align__(16) uint8_t smem[];
+  LoraSmem& sm = *reinterpret_cast<LoraSmem*>(smem);
+  int32_t *ids = sm.ids, *tok = sm.tok, *head = sm.head, *lead_count = sm.lead_count;
 
   cg::cluster_group cluster = cg::this_cluster();
   const int part = cluster.block_rank();
@@ -421,7 +496,7 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   if (rt < rts) {
     const int pieces = p.k >> 5, shares = LORA_CLUSTER * kparts, s = part * kparts + kp;
     const int g0 = (int)((int64_t)pieces * s / shares), g1 = (int)((int64_t)pieces * (s + 1) / shares);
-    float* to = hp + warp * 16 * kLoraTile;
+    float* to = sm.warp + warp * 16 * kLoraTile;
     if (cnt <= 8)
       lora_shrink<BF16, 1>(p, ad, rt, tok, cnt, g0, g1, to);
     else if (cnt <= 16)
@@ -431,31 +506,50 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   }
   __syncthreads();
   const int cols = cnt <= 8 ? 8 : (cnt <= 16 ? 16 : 32), cshift = cnt <= 8 ? 3 : (cnt <= 16 ? 4 : 5);
-  for (int i = tid; i < p.rank << cshift; i += LORA_THREADS) {
+  const int entries = p.rank << cshift;
+  for (int i = tid; i < entries; i += LORA_THREADS) {
     const int r = i >> cshift, c = i & (cols - 1);
-    const float* src = hp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * kLoraTile + c;
+    const float* src = sm.warp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * kLoraTile + c;
     float s = 0.f;
     for (int w = 0; w < kparts; ++w) s += src[w * 16 * kLoraTile];
-    h[r * kLoraTile + c] = s;
+    sm.h[i] = s;
   }
   cluster.sync();
 
   // ---- 2. the cluster's sum, as terms of the operand type --------------------------
+  // few entries: every block adds up all of them; more: each adds up an eighth
+  // and sends it to all
+  {
+    const bool all = entries <= 512;
+    const int quads = entries >> 2, i0 = all ? 0 : quads * part / LORA_CLUSTER;
+    const int i1 = all ? quads : quads * (part + 1) / LORA_CLUSTER;
+    for (int i = i0 + tid; i < i1; i += LORA_THREADS) {
+      float4 v[LORA_CLUSTER];
+#pragma unroll
+      for (int b = 0; b < LORA_CLUSTER; ++b) v[b] = reinterpret_cast<const float4*>(cluster.map_shared_rank(sm.h, b))[i];
+#pragma unroll
+      for (int b = 1; b < LORA_CLUSTER; ++b) v[0].x += v[b].x, v[0].y += v[b].y, v[0].z += v[b].z, v[0].w += v[b].w;
+      if (all) {
+        reinterpret_cast<float4*>(sm.total)[i] = v[0];
+      } else {
+#pragma unroll
+        for (int b = 0; b < LORA_CLUSTER; ++b) reinterpret_cast<float4*>(cluster.map_shared_rank(sm.total, b))[i] = v[0];
+      }
+    }
+    if (all)
+      __syncthreads();
+    else
+      cluster.sync();
+  }
   // one warp per token: lane l has ranks l, l + 32, ...
   const float sa = p.scale ? p.scale[ad] : 1.f;
   const int ranks = rts * 16;  // the last tile's missing ranks are zero terms
   for (int c = warp; c < cols; c += WARPS) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = j * 32 + lane;
-      if (r < p.rank && c < cnt) {
-        float part_h[LORA_CLUSTER];
-#pragma unroll
-        for (int b = 0; b < LORA_CLUSTER; ++b) part_h[b] = cluster.map_shared_rank(h, b)[r * kLoraTile + c];
-#pragma unroll
-        for (int b = 0; b < LORA_CLUSTER; ++b) v[j] += part_h[b];
-      }
+      v[j] = r < p.rank && c < cnt ? sm.total[(r << cshift) + c] : 0.f;
     }
     float up = 1.f;  // what the scaled terms are multiplied by
     if constexpr (!BF16) {
@@ -471,7 +565,7 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
         for (int j = 0; j < 4; ++j) v[j] *= down;
       }
     }
-    if (lane == 0) mul[c] = sa * up;
+    if (lane == 0) sm.mul[c] = sa * up;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = j * 32 + lane;
@@ -480,26 +574,30 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
 #pragma unroll
       for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
         const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
-        planes[(term * kLoraTile + c) * PLANE_STRIDE + r] = t;
+        sm.planes[(term * kLoraTile + c) * LoraSmem::PSTRIDE + r] = t;
         const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
         rest = fabsf(back) < INFINITY ? rest - back : 0.f;
       }
     }
   }
-  __syncthreads();
+  // before copies of y take the place of the sums, and before a block leaves,
+  // the others have read its h (those who got the sums sent have already)
+  if (entries <= 512)
+    cluster.sync();
+  else
+    __syncthreads();
 
   // ---- 3. out = y + s B h over this block's share of n -------------------------------
   const int groups = (p.n + 31) >> 5;
-  const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER), e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
-  for (int e = e0 + warp; e < e1; e += WARPS) {
-    if (cnt <= 8)
-      lora_expand<BF16, VEC, 1>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
-    else if (cnt <= 16)
-      lora_expand<BF16, VEC, 2>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
-    else
-      lora_expand<BF16, VEC, 4>(p, ad, e * 32, tok, cnt, planes, PLANE_STRIDE, mul);
-  }
-  cluster.sync();  // the other blocks have read this one's h
+  const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER) + warp, e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
+  uint8_t* ring = sm.ring + warp * 2 * kLoraTile * 128;
+  if (cnt <= 8)
+    lora_expand<BF16, VEC, 1, 2, 2, false>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
+  else if (cnt <= 16)
+    lora_expand<BF16, VEC, 2, 1, 4, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
+  else
+    lora_expand<BF16, VEC, 4, 1, 4, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
+  if (VEC) cp_async_wait<0>();
 }
 
 }  // namespace tq

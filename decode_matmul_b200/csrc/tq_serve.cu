@@ -168,6 +168,19 @@ size_t lora_ws_bytes(int32_t m) {
   return kCounterBytes + (m > tq::kLoraInBlock ? (size_t)tq::kPlanInts * sizeof(int32_t) : 0);
 }
 
+template <bool BF16, bool VEC>
+int lora_launch(dim3 grid, const tq::LoraParams& p, cudaStream_t stream) {
+  auto kern = tq::lora_kernel<BF16, VEC>;
+  static int configured[kMaxDevices];
+  int dev = 0;
+  TQ_CUDA(cudaGetDevice(&dev));
+  if (!configured[dev]) {
+    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(tq::LoraSmem)));
+    configured[dev] = 1;
+  }
+  return launch(kern, grid, dim3(tq::LORA_THREADS), sizeof(tq::LoraSmem), stream, p);
+}
+
 }  // namespace
 
 extern "C" {
@@ -324,13 +337,10 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   // tiles: every adapter (and the tokens without one) adds at most one that is not full
   int64_t tiles = (int64_t)(m / tq::kLoraTile) + lora->n_adapters + 1;
   if (tiles > m) tiles = m;
-  const dim3 grid((unsigned)tiles * tq::LORA_CLUSTER), block(tq::LORA_THREADS);
+  const dim3 grid((unsigned)tiles * tq::LORA_CLUSTER);
   const bool vec = aligned16(y_d) && aligned16(out_d) && y_stride % 4 == 0 && out_stride % 4 == 0;
-  if (lora->dtype == TQ_BF16)
-    return vec ? launch(tq::lora_kernel<true, true>, grid, block, 0, s, p)
-               : launch(tq::lora_kernel<true, false>, grid, block, 0, s, p);
-  return vec ? launch(tq::lora_kernel<false, true>, grid, block, 0, s, p)
-             : launch(tq::lora_kernel<false, false>, grid, block, 0, s, p);
+  if (lora->dtype == TQ_BF16) return vec ? lora_launch<true, true>(grid, p, s) : lora_launch<true, false>(grid, p, s);
+  return vec ? lora_launch<false, true>(grid, p, s) : lora_launch<false, false>(grid, p, s);
 }
 
 }  // extern "C"
