@@ -22,6 +22,7 @@
 #include <cooperative_groups.h>
 
 #include "tq_attn.cuh"
+#include "tq_umma.cuh"
 
 namespace tq {
 
@@ -40,6 +41,16 @@ struct LoraParams {
   int32_t* plan;  // workspace (m > kLoraInBlock): tiles, perm [4096], first [4097]
   int32_t* status;
 };
+
+// 16 consecutive 32-bit TMEM columns of this thread's lane (warp-collective)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
 
 constexpr int LORA_THREADS = 256;
 constexpr int LORA_CLUSTER = 8;
@@ -231,35 +242,17 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   }
 }
 
-// Step 3 for NT columns of 8 tokens: this warp's groups of 32 features, e0,
-// e0 + step, ... below e1.  GN groups are worked on together; B is loaded
-// AHEAD steps of 16 ranks at a time, before the steps in hand are multiplied.
-// RING: y comes through this warp's two buffers in shared memory, copied a
-// round ahead (with 32 tokens its registers would not leave room to have the
-// next group's loads in flight).
-template <bool BF16, bool VEC, int NT, int GN, int AHEAD, bool RING>
-__device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int e0, int e1, int step, const int32_t* tok,
-                                            int cnt, const uint16_t* planes, int pstride, const float* mul, uint8_t* ring) {
-  static_assert(!RING || (VEC && GN == 1), "ring");
+// Step 3 for up to 8 tokens: this warp's groups of 32 features, e0, e0 + step,
+// ... below e1, two at a time with all their loads in flight (B 32 ranks at a
+// time, the next while these are multiplied).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, int e0, int e1, int step, const int32_t* tok,
+                                             int cnt, const uint16_t* planes, int pstride, const float* mul) {
+  constexpr int GN = 2, AHEAD = 2;
   constexpr int TERMS = BF16 ? 3 : 2;
-  constexpr int STAGE = NT * 8 * 128;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
   const uint16_t* bp = static_cast<const uint16_t*>(p.b) + (int64_t)ad * p.n * p.rank + q * 4;
-  const uint32_t ring_u = RING ? smem_u32(ring) : 0;
-  // row c of a stage is token c's 8 chunks of 4 features, chunk i at i ^ ((c >> 1) & 3) * 2
-  auto fetch = [&](int e, int stage) {
-#pragma unroll
-    for (int i = 0; i < NT * 2; ++i) {
-      const int c = i * 4 + (lane >> 3), ch = lane & 7, f = e * 32 + ch * 4;
-      const bool in = e < e1 && c < cnt && f + 4 <= p.n;
-      const float* src = in ? p.y + tok[c] * p.y_stride + f : p.y;
-      cp_async16(ring_u + stage * STAGE + c * 128 + (ch ^ (((c >> 1) & 3) * 2)) * 16, src, in);
-    }
-    cp_async_commit();
-  };
-  int stage = 0;
-  if (RING) fetch(e0, 0);
   for (int e = e0; e < e1; e += GN * step) {
     uint2 b[GN][AHEAD][4];
     auto load_b = [&](int r0) {
@@ -279,136 +272,213 @@ __device__ __forceinline__ void lora_expand(const LoraParams& p, int32_t ad, int
       }
     };
     load_b(0);
-    if (RING) fetch(e + step, stage ^ 1);
-    float4 yv[GN][NT][2];
-    if (!RING) {
+    float4 yv[GN][2];
 #pragma unroll
-      for (int j = 0; j < GN; ++j) {
-        const int f = (e + j * step) * 32 + 4 * g;
+    for (int j = 0; j < GN; ++j) {
+      const int f = (e + j * step) * 32 + 4 * g;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = nt * 8 + q * 2 + i;
-            float4& v = yv[j][nt][i];
-            v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (e + j * step < e1 && c < cnt && f < p.n) {
-              const float* src = p.y + tok[c] * p.y_stride + f;
-              if (VEC && f + 4 <= p.n) {
-                v = *reinterpret_cast<const float4*>(src);
-              } else {
-                v.x = src[0];
-                if (f + 1 < p.n) v.y = src[1];
-                if (f + 2 < p.n) v.z = src[2];
-                if (f + 3 < p.n) v.w = src[3];
-              }
-            }
+      for (int i = 0; i < 2; ++i) {
+        const int c = q * 2 + i;
+        float4& v = yv[j][i];
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e + j * step < e1 && c < cnt && f < p.n) {
+          const float* src = p.y + tok[c] * p.y_stride + f;
+          if (VEC && f + 4 <= p.n) {
+            v = *reinterpret_cast<const float4*>(src);
+          } else {
+            v.x = src[0];
+            if (f + 1 < p.n) v.y = src[1];
+            if (f + 2 < p.n) v.z = src[2];
+            if (f + 3 < p.n) v.w = src[3];
           }
+        }
       }
     }
-    float acc[GN][2][NT][4];
+    float acc[GN][2][4];
 #pragma unroll
     for (int j = 0; j < GN; ++j)
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[j][mt][nt][i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[j][mt][i] = 0.f;
     for (int r0 = 0; r0 < p.rank; r0 += 16 * AHEAD) {
+      uint2 now[GN][AHEAD][4];
+#pragma unroll
+      for (int j = 0; j < GN; ++j)
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now[j][u][i] = b[j][u][i];
+      if (r0 + 16 * AHEAD < p.rank) load_b(r0 + 16 * AHEAD);
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
         const int r = r0 + u * 16;
         if (r >= p.rank) break;
-        uint32_t m0[GN][4], m1[GN][4];
 #pragma unroll
-        for (int j = 0; j < GN; ++j) {
-          m0[j][0] = b[j][u][0].x, m0[j][1] = b[j][u][1].x, m0[j][2] = b[j][u][0].y, m0[j][3] = b[j][u][1].y;
-          m1[j][0] = b[j][u][2].x, m1[j][1] = b[j][u][3].x, m1[j][2] = b[j][u][2].y, m1[j][3] = b[j][u][3].y;
-        }
+        for (int term = 0; term < TERMS; ++term) {
+          const uint2 h = *reinterpret_cast<const uint2*>(planes + (term * 8 + g) * pstride + r + q * 4);
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 h = *reinterpret_cast<const uint2*>(planes + ((term * kLoraTile) + nt * 8 + g) * pstride + r + q * 4);
-#pragma unroll
-            for (int j = 0; j < GN; ++j) {
-              mma16<BF16>(acc[j][0][nt], m0[j], h.x, h.y);
-              mma16<BF16>(acc[j][1][nt], m1[j], h.x, h.y);
-            }
+          for (int j = 0; j < GN; ++j) {
+            const uint32_t m0[4] = {now[j][u][0].x, now[j][u][1].x, now[j][u][0].y, now[j][u][1].y};
+            const uint32_t m1[4] = {now[j][u][2].x, now[j][u][3].x, now[j][u][2].y, now[j][u][3].y};
+            mma16<BF16>(acc[j][0], m0, h.x, h.y);
+            mma16<BF16>(acc[j][1], m1, h.x, h.y);
           }
+        }
       }
-      if (r0 + 16 * AHEAD < p.rank) load_b(r0 + 16 * AHEAD);
-    }
-    if (RING) {
-      cp_async_wait<1>();
-      __syncwarp();
     }
 #pragma unroll
     for (int j = 0; j < GN; ++j) {
       const int f = (e + j * step) * 32 + 4 * g;
       if (e + j * step >= e1) break;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = nt * 8 + q * 2 + i;
-          if (c >= cnt || f >= p.n) continue;
-          float4 v = yv[j][nt][i];
-          if (RING) {
-            v = *reinterpret_cast<const float4*>(ring + stage * STAGE + c * 128 + (g ^ (q * 2)) * 16);
-            if (f + 4 > p.n) {  // the last features of an odd n were not copied
-              const float* src = p.y + tok[c] * p.y_stride + f;
-              v.x = src[0];
-              if (f + 1 < p.n) v.y = src[1];
-              if (f + 2 < p.n) v.z = src[2];
-            }
-          }
-          const float s = mul[c];
-          v.x = fmaf(acc[j][0][nt][i], s, v.x);
-          v.y = fmaf(acc[j][0][nt][2 + i], s, v.y);
-          v.z = fmaf(acc[j][1][nt][i], s, v.z);
-          v.w = fmaf(acc[j][1][nt][2 + i], s, v.w);
-          float* dst = p.out + tok[c] * p.out_stride + f;
-          if (VEC && f + 4 <= p.n) {
-            *reinterpret_cast<float4*>(dst) = v;
-          } else {
-            dst[0] = v.x;
-            if (f + 1 < p.n) dst[1] = v.y;
-            if (f + 2 < p.n) dst[2] = v.z;
-            if (f + 3 < p.n) dst[3] = v.w;
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int c = q * 2 + i;
+        if (c >= cnt || f >= p.n) continue;
+        const float s = mul[c];
+        float4 v = yv[j][i];
+        v.x = fmaf(acc[j][0][i], s, v.x);
+        v.y = fmaf(acc[j][0][2 + i], s, v.y);
+        v.z = fmaf(acc[j][1][i], s, v.z);
+        v.w = fmaf(acc[j][1][2 + i], s, v.w);
+        float* dst = p.out + tok[c] * p.out_stride + f;
+        if (VEC && f + 4 <= p.n) {
+          *reinterpret_cast<float4*>(dst) = v;
+        } else {
+          dst[0] = v.x;
+          if (f + 1 < p.n) dst[1] = v.y;
+          if (f + 2 < p.n) dst[2] = v.z;
+          if (f + 3 < p.n) dst[3] = v.w;
         }
+      }
     }
-    stage ^= 1;
-    if (RING) __syncwarp();  // the buffer is read before it is filled again
   }
 }
 
-// Shared memory of a block.  The copies of y (step 3) take the place of the
-// sums of A x (steps 1 and 2).
+// Shared memory of a block.  In step 3 the tiles of B (9 to 32 tokens) take
+// the place of the sums of A x (steps 1 and 2).
 struct LoraSmem {
   static constexpr int PSTRIDE = 128 + 16;  // a token's terms, 8 words past a multiple of 32 (no bank conflicts)
   static constexpr int WARPS = LORA_THREADS / 32;
-  int32_t ids[kLoraInBlock], tok[kLoraTile], head[4], lead_count[WARPS];
-  float mul[kLoraTile];
-  uint16_t planes[3 * kLoraTile * PSTRIDE];  // [term][token][rank]
-  union alignas(16) {
+  static constexpr int PANEL_B = 128 * 128;         // 128 features x 64 ranks
+  static constexpr int PANEL_H = kLoraTile * 128;   // 32 tokens x 64 ranks
+  union {
     struct {
       float h[128 * kLoraTile];      // the block's sum: [rank][token]
       float total[128 * kLoraTile];  // the cluster's
       float warp[WARPS * 16 * kLoraTile];
     };
-    uint8_t ring[WARPS * 2 * kLoraTile * 128];
+    uint8_t b[2][2 * PANEL_B];  // two tiles of 128 features, up to 128 ranks
   };
+  union {
+    uint16_t planes[3 * 8 * PSTRIDE];  // up to 8 tokens: [term][token][rank]
+    uint8_t terms[3][2 * PANEL_H];     // more: operand tiles
+  };
+  int64_t yoff[kLoraTile], ooff[kLoraTile];  // the tokens' rows of y and out
+  uint64_t bar[2];
+  int32_t ids[kLoraInBlock], tok[kLoraTile], head[4], lead_count[WARPS];
+  float mul[kLoraTile];
+  uint32_t tmem;
 };
+
+// Step 3 for 9 to 32 tokens, on the tcgen05 tensor cores: D [128 features][32
+// tokens] = B [128][rank] (terms of h)^T.  Read out of shared memory by the
+// tensor core, the operands cost the threads nothing: with warp MMAs their
+// fragments (and the addresses of 8 tokens' y per thread) took 1350
+// instructions per 32 x 32 outputs and 54 us of 1000 tokens x 19456 features
+// at rank 64.  The next tile of B is copied and its y loaded while this one is
+// multiplied; each thread has one feature and 16 tokens, so a warp's accesses
+// of y and out are 128 bytes in a row at any alignment.
+template <bool BF16>
+__device__ __forceinline__ void lora_expand32(const LoraParams& p, int32_t ad, int cnt, int part, LoraSmem& sm) {
+  constexpr int TERMS = BF16 ? 3 : 2;
+  constexpr uint32_t IDESC = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((kLoraTile >> 3) << 17) | ((128 >> 4) << 24);
+  constexpr int COLS = kLoraTile / 2;  // tokens of a thread
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int panels = (p.rank + 63) >> 6, steps = (p.rank + 15) >> 4;
+  const int tiles = (p.n + 127) >> 7;
+  const int t0 = tiles * part / LORA_CLUSTER, t1 = tiles * (part + 1) / LORA_CLUSTER;
+  const uint32_t bar = smem_u32(sm.bar), tmem = sm.tmem;
+  const uint16_t* bsrc = static_cast<const uint16_t*>(p.b) + (int64_t)ad * p.n * p.rank;
+  // rows of 64 ranks are 128 bytes, 16-byte chunk i of row r at i ^ (r & 7)
+  // (the 128-byte swizzle); ranks up to the last step of 16 that are not there
+  // are zeros
+  auto fetch = [&](int t) {
+    const uint32_t dst = smem_u32(sm.b[t & 1]);
+    for (int pn = 0; pn < panels; ++pn) {
+      const int chunks = min(8, steps * 2 - pn * 8);
+      const int ch = tid & 7;
+      if (ch < chunks) {
+        const int r = pn * 64 + ch * 8;
+#pragma unroll
+        for (int i = 0; i < 128 * 8 / LORA_THREADS; ++i) {
+          const int row = i * (LORA_THREADS / 8) + (tid >> 3), f = t * 128 + row;
+          const bool in = f < p.n && r < p.rank;
+          cp_async16(dst + pn * LoraSmem::PANEL_B + row * 128 + ((ch ^ (row & 7)) << 4),
+                     in ? bsrc + (int64_t)f * p.rank + r : bsrc, in);
+        }
+      }
+    }
+  };
+  const int c0 = (warp >> 2) * COLS;
+  const int row = (warp & 3) * 32 + lane;
+  float yv[COLS];
+  auto load_y = [&](int t) {
+    const int f = t * 128 + row;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) yv[j] = c0 + j < cnt && f < p.n && t < t1 ? p.y[sm.yoff[c0 + j] + f] : 0.f;
+  };
+  if (t0 < t1) fetch(t0);
+  cp_async_commit();
+  load_y(t0);
+  bool good = true;
+  for (int t = t0; t < t1; ++t) {
+    if (t + 1 < t1) fetch(t + 1);  // into the buffer whose products the previous round waited for
+    cp_async_commit();
+    cp_async_wait<1>();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    const int it = t - t0;
+    const uint32_t d = tmem + (it & 1) * kLoraTile;
+    if (tid == 0) {
+      tc_fence_after();
+      for (int k = 0; k < steps; ++k) {
+        const uint64_t a = umma_smem_desc(smem_u32(sm.b[t & 1]) + (k >> 2) * LoraSmem::PANEL_B + (k & 3) * 32);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+          umma_f16(d, a, umma_smem_desc(smem_u32(sm.terms[term]) + (k >> 2) * LoraSmem::PANEL_H + (k & 3) * 32), IDESC,
+                   k + term > 0);
+      }
+      umma_commit(bar + 8 * (it & 1));
+    }
+    float v[COLS];
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) v[j] = yv[j];
+    load_y(t + 1);
+    // a wait that runs out (it cannot in a healthy launch) leaves the outputs undefined and says so
+    good = __all_sync(0xffffffffu, mbar_wait(bar + 8 * (it & 1), (it >> 1) & 1, 1u << 21));
+    if (!good) {
+      if (lane == 0) atomicExch(p.status, UM_TIMEOUT_STATUS);
+      continue;
+    }
+    tc_fence_after();
+    uint32_t acc[COLS];
+    tmem_ld16(d + ((uint32_t)((warp & 3) * 32) << 16) + c0, acc);
+    const int f = t * 128 + row;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j)
+      if (c0 + j < cnt && f < p.n) p.out[sm.ooff[c0 + j] + f] = fmaf(__uint_as_float(acc[j]), sm.mul[c0 + j], v[j]);
+  }
+  cp_async_wait<0>();
+}
 
 template <bool BF16, bool VEC>
 __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 2)
     lora_kernel(const __grid_constant__ LoraParams p) {
   constexpr int WARPS = LORA_THREADS / 32;
   extern __shared__ __align__(16) uint8_t smem[];
-  LoraSmem& sm = *reinterpret_cast<LoraSmem*>(smem);
+  LoraSmem& sm = *reinterpret_cast<LoraSmem*>(smem + (-smem_u32(smem) & 1023u));  // the operand tiles are aligned to 1 KB
   int32_t *ids = sm.ids, *tok = sm.tok, *head = sm.head, *lead_count = sm.lead_count;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -417,7 +487,6 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   pdl_wait();
-  pdl_launch_dependents();
 
   // ---- the tile's tokens -------------------------------------------------------
   int cnt;
@@ -473,6 +542,7 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   }
 
   if (ad < 0) {  // no adapter: y as it is
+    if (warp == 0) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     if (p.out != p.y)
       for (int c = 0; c < cnt; ++c) {
         const float* src = p.y + tok[c] * p.y_stride;
@@ -488,6 +558,32 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
       }
     return;
   }
+
+  const bool wide = cnt > 8;  // step 3 on the tcgen05 tensor cores
+  // every block gives up its right to allocate tensor memory at once: until it
+  // does, no second block of this kernel starts on its SM (64 tokens of 24
+  // adapters: 34 us with one block per SM at a time, 20 us with two)
+  if (!wide && warp == 0) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  if (wide) {
+    if (warp == 0) {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(64u));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    if (tid == 32) {
+      mbar_init(smem_u32(sm.bar), 1);
+      mbar_init(smem_u32(sm.bar) + 8, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (tid >= 64 && tid < 64 + cnt) {
+      sm.yoff[tid - 64] = tok[tid - 64] * p.y_stride;
+      sm.ooff[tid - 64] = tok[tid - 64] * p.out_stride;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  // only now: the next kernel may take tensor memory before it waits for this one
+  pdl_launch_dependents();
 
   // ---- 1. h = A x over this block's share of k -----------------------------------
   const int rts = (p.rank + 15) >> 4;         // 16-row tiles of A
@@ -544,7 +640,8 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   // one warp per token: lane l has ranks l, l + 32, ...
   const float sa = p.scale ? p.scale[ad] : 1.f;
   const int ranks = rts * 16;  // the last tile's missing ranks are zero terms
-  for (int c = warp; c < cols; c += WARPS) {
+  // (with more than 8 tokens the operand tile's 32 rows, all of them)
+  for (int c = warp; c < (wide ? kLoraTile : 8); c += WARPS) {
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -574,7 +671,11 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
 #pragma unroll
       for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
         const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
-        sm.planes[(term * kLoraTile + c) * LoraSmem::PSTRIDE + r] = t;
+        if (!wide)
+          sm.planes[(term * 8 + c) * LoraSmem::PSTRIDE + r] = t;
+        else
+          *reinterpret_cast<uint16_t*>(sm.terms[term] + (r >> 6) * LoraSmem::PANEL_H + c * 128 +
+                                       ((((r >> 3) & 7) ^ (c & 7)) << 4) + (r & 7) * 2) = t;
         const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
         rest = fabsf(back) < INFINITY ? rest - back : 0.f;
       }
@@ -588,16 +689,20 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
     __syncthreads();
 
   // ---- 3. out = y + s B h over this block's share of n -------------------------------
-  const int groups = (p.n + 31) >> 5;
-  const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER) + warp, e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
-  uint8_t* ring = sm.ring + warp * 2 * kLoraTile * 128;
-  if (cnt <= 8)
-    lora_expand<BF16, VEC, 1, 2, 2, false>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
-  else if (cnt <= 16)
-    lora_expand<BF16, VEC, 2, 1, 4, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
-  else
-    lora_expand<BF16, VEC, 4, 1, 4, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul, ring);
-  if (VEC) cp_async_wait<0>();
+  if (!wide) {
+    const int groups = (p.n + 31) >> 5;
+    const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER) + warp;
+    const int e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
+    lora_expand8<BF16, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul);
+    return;
+  }
+  lora_expand32<BF16>(p, ad, cnt, part, sm);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem), "r"(64u));
+  }
 }
 
 }  // namespace tq

@@ -175,10 +175,10 @@ int lora_launch(dim3 grid, const tq::LoraParams& p, cudaStream_t stream) {
   int dev = 0;
   TQ_CUDA(cudaGetDevice(&dev));
   if (!configured[dev]) {
-    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(tq::LoraSmem)));
+    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(tq::LoraSmem) + 1024));
     configured[dev] = 1;
   }
-  return launch(kern, grid, dim3(tq::LORA_THREADS), sizeof(tq::LoraSmem), stream, p);
+  return launch(kern, grid, dim3(tq::LORA_THREADS), sizeof(tq::LoraSmem) + 1024, stream, p);
 }
 
 }  // namespace
