@@ -3,17 +3,25 @@
 //   out[t] = y[t] + s_a B_a (A_a x_t),   a = the token's adapter
 //
 // Bound: memory.  The adapters that are used, x and y are read once and out is
-// written once; the products are a few per cent of the tensor rate.
-// Tokens of one adapter are worked on together, up to 32 in a tile (stable
-// order), by one cluster of eight blocks:
+// written once; the products are a few per cent of the tensor rate.  Tokens of
+// one adapter are worked on together, so that its A and B are read once for
+// all of them.
+//
+// Up to 256 tokens (decoding), one launch: tiles of up to 8 tokens, each by a
+// cluster of eight blocks:
 //   1. h = A x: the cluster's warps split k (and the 16-row tiles of A); each
 //      reads its pieces of A and x straight into MMA fragments (16-byte loads;
 //      the order of k inside an MMA is permuted alike for both),
-//   2. the blocks' sums of h are exchanged through distributed shared memory,
-//      so no second launch and no trip through global memory is needed,
+//   2. the blocks' sums of h are read through distributed shared memory: no
+//      second launch, no trip through global memory,
 //   3. each block takes an eighth of the n output features: B as the 16-row
 //      operand, tokens as the 8-wide one, 32 features in an order that gives a
 //      thread four neighbours (16-byte accesses of y and out).
+// More tokens (prompts), three launches: the tokens are grouped, h is summed
+// over splits of k into the workspace, and tiles of 128 features x 32 tokens
+// are multiplied on the tcgen05 tensor cores, whose operands cost the threads
+// nothing (with warp MMAs the fragments and addresses took 1350 instructions
+// per 32 x 32 outputs).
 // A x keeps binary32 accuracy through the second product: it enters as three
 // bf16 terms (24 bits), or as two fp16 terms of a token's h scaled by a power
 // of two (22 bits of its largest element).
@@ -38,7 +46,10 @@ struct LoraParams {
   float* out;          // rows of out_stride
   int64_t y_stride, out_stride;
   int32_t n_adapters, rank, n, k, m;
-  int32_t* plan;  // workspace (m > kLoraInBlock): tiles, perm [4096], first [4097]
+  // workspace, m > kLoraInBlock
+  int32_t* plan;    // tiles, perm [4096], first [4097]
+  float* h;         // [splits][m, in perm's order][rank]
+  int32_t splits;   // of k
   int32_t* status;
 };
 
@@ -54,8 +65,9 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 
 constexpr int LORA_THREADS = 256;
 constexpr int LORA_CLUSTER = 8;
-constexpr int kLoraTile = 32;      // tokens of a tile
 constexpr int kLoraInBlock = 256;  // up to this many tokens each block groups them for itself
+constexpr int kLoraSmall = 8;      // tokens of a tile up to kLoraInBlock, and beyond
+constexpr int kLoraTile = 32;
 constexpr int kLoraMaxM = 4096;
 constexpr int kPlanPerm = 4, kPlanFirst = kPlanPerm + kLoraMaxM, kPlanInts = kPlanFirst + kLoraMaxM + 4;
 
@@ -153,7 +165,12 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
   __syncthreads();
   int32_t prev = __shfl_up_sync(0xffffffffu, before, 1);
   if (lane == 0) prev = -1;
-  for (int w = 0; w < warp; ++w) prev = max(prev, warp_max[w]);
+  {
+    int32_t v = lane < warp ? warp_max[lane] : -1;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+    prev = max(prev, v);
+  }
   int32_t lead = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -172,11 +189,13 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int32_t at_tile = incl - lead, total = 0;
-  for (int w = 0; w < 32; ++w) {
-    if (w < warp) at_tile += warp_sum[w];
-    total += warp_sum[w];
+  int32_t total = warp_sum[lane], prior = lane < warp ? total : 0;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, d);
+    prior += __shfl_xor_sync(0xffffffffu, prior, d);
   }
+  int32_t at_tile = incl - lead + prior;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i0 + i;
@@ -190,7 +209,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
 
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-// Step 1 for NT columns of 8 tokens: this warp's sum over its k pieces.
+// A x for NT columns of 8 tokens: this warp's sum over its pieces of k, to
+// hp [16 ranks][8 NT].
 template <bool BF16, int NT>
 __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int rt, const int32_t* tok, int cnt, int g0,
                                             int g1, float* hp) {
@@ -237,8 +257,8 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   // [rank in tile][token]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    *reinterpret_cast<float2*>(hp + g * kLoraTile + nt * 8 + q * 2) = make_float2(acc[nt][0], acc[nt][1]);
-    *reinterpret_cast<float2*>(hp + (g + 8) * kLoraTile + nt * 8 + q * 2) = make_float2(acc[nt][2], acc[nt][3]);
+    *reinterpret_cast<float2*>(hp + g * NT * 8 + nt * 8 + q * 2) = make_float2(acc[nt][0], acc[nt][1]);
+    *reinterpret_cast<float2*>(hp + (g + 8) * NT * 8 + nt * 8 + q * 2) = make_float2(acc[nt][2], acc[nt][3]);
   }
 }
 
@@ -355,131 +375,52 @@ __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, in
   }
 }
 
-// Shared memory of a block.  In step 3 the tiles of B (9 to 32 tokens) take
-// the place of the sums of A x (steps 1 and 2).
-struct LoraSmem {
-  static constexpr int PSTRIDE = 128 + 16;  // a token's terms, 8 words past a multiple of 32 (no bank conflicts)
-  static constexpr int WARPS = LORA_THREADS / 32;
-  static constexpr int PANEL_B = 128 * 128;         // 128 features x 64 ranks
-  static constexpr int PANEL_H = kLoraTile * 128;   // 32 tokens x 64 ranks
-  union {
-    struct {
-      float h[128 * kLoraTile];      // the block's sum: [rank][token]
-      float total[128 * kLoraTile];  // the cluster's
-      float warp[WARPS * 16 * kLoraTile];
-    };
-    uint8_t b[2][2 * PANEL_B];  // two tiles of 128 features, up to 128 ranks
-  };
-  union {
-    uint16_t planes[3 * 8 * PSTRIDE];  // up to 8 tokens: [term][token][rank]
-    uint8_t terms[3][2 * PANEL_H];     // more: operand tiles
-  };
-  int64_t yoff[kLoraTile], ooff[kLoraTile];  // the tokens' rows of y and out
-  uint64_t bar[2];
-  int32_t ids[kLoraInBlock], tok[kLoraTile], head[4], lead_count[WARPS];
-  float mul[kLoraTile];
-  uint32_t tmem;
-};
-
-// Step 3 for 9 to 32 tokens, on the tcgen05 tensor cores: D [128 features][32
-// tokens] = B [128][rank] (terms of h)^T.  Read out of shared memory by the
-// tensor core, the operands cost the threads nothing: with warp MMAs their
-// fragments (and the addresses of 8 tokens' y per thread) took 1350
-// instructions per 32 x 32 outputs and 54 us of 1000 tokens x 19456 features
-// at rank 64.  The next tile of B is copied and its y loaded while this one is
-// multiplied; each thread has one feature and 16 tokens, so a warp's accesses
-// of y and out are 128 bytes in a row at any alignment.
-template <bool BF16>
-__device__ __forceinline__ void lora_expand32(const LoraParams& p, int32_t ad, int cnt, int part, LoraSmem& sm) {
-  constexpr int TERMS = BF16 ? 3 : 2;
-  constexpr uint32_t IDESC = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((kLoraTile >> 3) << 17) | ((128 >> 4) << 24);
-  constexpr int COLS = kLoraTile / 2;  // tokens of a thread
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int panels = (p.rank + 63) >> 6, steps = (p.rank + 15) >> 4;
-  const int tiles = (p.n + 127) >> 7;
-  const int t0 = tiles * part / LORA_CLUSTER, t1 = tiles * (part + 1) / LORA_CLUSTER;
-  const uint32_t bar = smem_u32(sm.bar), tmem = sm.tmem;
-  const uint16_t* bsrc = static_cast<const uint16_t*>(p.b) + (int64_t)ad * p.n * p.rank;
-  // rows of 64 ranks are 128 bytes, 16-byte chunk i of row r at i ^ (r & 7)
-  // (the 128-byte swizzle); ranks up to the last step of 16 that are not there
-  // are zeros
-  auto fetch = [&](int t) {
-    const uint32_t dst = smem_u32(sm.b[t & 1]);
-    for (int pn = 0; pn < panels; ++pn) {
-      const int chunks = min(8, steps * 2 - pn * 8);
-      const int ch = tid & 7;
-      if (ch < chunks) {
-        const int r = pn * 64 + ch * 8;
+// h of one token as terms of the operand type: lane l has ranks l, l + 32, ...
+// in v; put(term, rank, bits) takes them.  Returns what the scaled terms are to
+// be multiplied by.
+template <bool BF16, class Put>
+__device__ __forceinline__ float lora_terms(float v[4], int ranks, Put put) {
+  const int lane = threadIdx.x & 31;
+  float up = 1.f;
+  if constexpr (!BF16) {
+    float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
-        for (int i = 0; i < 128 * 8 / LORA_THREADS; ++i) {
-          const int row = i * (LORA_THREADS / 8) + (tid >> 3), f = t * 128 + row;
-          const bool in = f < p.n && r < p.rank;
-          cp_async16(dst + pn * LoraSmem::PANEL_B + row * 128 + ((ch ^ (row & 7)) << 4),
-                     in ? bsrc + (int64_t)f * p.rank + r : bsrc, in);
-        }
-      }
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    // the largest element goes to [2^9, 2^10)
+    const int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;
+    if (e > -110 && e < 120) {
+      up = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
+      const float down = __uint_as_float((uint32_t)(9 - e + 127) << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= down;
     }
-  };
-  const int c0 = (warp >> 2) * COLS;
-  const int row = (warp & 3) * 32 + lane;
-  float yv[COLS];
-  auto load_y = [&](int t) {
-    const int f = t * 128 + row;
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) yv[j] = c0 + j < cnt && f < p.n && t < t1 ? p.y[sm.yoff[c0 + j] + f] : 0.f;
-  };
-  if (t0 < t1) fetch(t0);
-  cp_async_commit();
-  load_y(t0);
-  bool good = true;
-  for (int t = t0; t < t1; ++t) {
-    if (t + 1 < t1) fetch(t + 1);  // into the buffer whose products the previous round waited for
-    cp_async_commit();
-    cp_async_wait<1>();
-    fence_async_smem();
-    tc_fence_before();
-    __syncthreads();
-    const int it = t - t0;
-    const uint32_t d = tmem + (it & 1) * kLoraTile;
-    if (tid == 0) {
-      tc_fence_after();
-      for (int k = 0; k < steps; ++k) {
-        const uint64_t a = umma_smem_desc(smem_u32(sm.b[t & 1]) + (k >> 2) * LoraSmem::PANEL_B + (k & 3) * 32);
-#pragma unroll
-        for (int term = 0; term < TERMS; ++term)
-          umma_f16(d, a, umma_smem_desc(smem_u32(sm.terms[term]) + (k >> 2) * LoraSmem::PANEL_H + (k & 3) * 32), IDESC,
-                   k + term > 0);
-      }
-      umma_commit(bar + 8 * (it & 1));
-    }
-    float v[COLS];
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) v[j] = yv[j];
-    load_y(t + 1);
-    // a wait that runs out (it cannot in a healthy launch) leaves the outputs undefined and says so
-    good = __all_sync(0xffffffffu, mbar_wait(bar + 8 * (it & 1), (it >> 1) & 1, 1u << 21));
-    if (!good) {
-      if (lane == 0) atomicExch(p.status, UM_TIMEOUT_STATUS);
-      continue;
-    }
-    tc_fence_after();
-    uint32_t acc[COLS];
-    tmem_ld16(d + ((uint32_t)((warp & 3) * 32) << 16) + c0, acc);
-    const int f = t * 128 + row;
-#pragma unroll
-    for (int j = 0; j < COLS; ++j)
-      if (c0 + j < cnt && f < p.n) p.out[sm.ooff[c0 + j] + f] = fmaf(__uint_as_float(acc[j]), sm.mul[c0 + j], v[j]);
   }
-  cp_async_wait<0>();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = j * 32 + lane;
+    if (r >= ranks) continue;
+    float rest = v[j];
+#pragma unroll
+    for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
+      const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
+      put(term, r, t);
+      const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
+      rest = fabsf(back) < INFINITY ? rest - back : 0.f;
+    }
+  }
+  return up;
 }
 
 template <bool BF16, bool VEC>
 __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 2)
     lora_kernel(const __grid_constant__ LoraParams p) {
-  constexpr int WARPS = LORA_THREADS / 32;
-  extern __shared__ __align__(16) uint8_t smem[];
-  LoraSmem& sm = *reinterpret_cast<LoraSmem*>(smem + (-smem_u32(smem) & 1023u));  // the operand tiles are aligned to 1 KB
-  int32_t *ids = sm.ids, *tok = sm.tok, *head = sm.head, *lead_count = sm.lead_count;
+  constexpr int WARPS = LORA_THREADS / 32, COLS = kLoraSmall;
+  constexpr int PSTRIDE = 128 + 16;  // a token's terms, 8 words past a multiple of 32 (no bank conflicts)
+  __shared__ __align__(16) int32_t ids[kLoraInBlock];
+  __shared__ int32_t tok[COLS], head[2], lead_count[WARPS];
+  __shared__ float mul[COLS];
+  __shared__ __align__(16) float h[128 * COLS], total[128 * COLS], hp[WARPS * 16 * COLS];  // [rank][token]
+  __shared__ __align__(16) uint16_t planes[3 * COLS * PSTRIDE];                            // [term][token][rank]
 
   cg::cluster_group cluster = cg::this_cluster();
   const int part = cluster.block_rank();
@@ -487,221 +428,392 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   pdl_wait();
+  pdl_launch_dependents();
 
-  // ---- the tile's tokens -------------------------------------------------------
-  int cnt;
-  int32_t ad;
-  if (p.m > kLoraInBlock) {
-    if (tile >= p.plan[0]) return;  // the whole cluster
-    const int i0 = p.plan[kPlanFirst + tile];
-    cnt = p.plan[kPlanFirst + tile + 1] - i0;
-    if (tid < cnt) tok[tid] = p.plan[kPlanPerm + i0 + tid];
+  // ---- the tile's tokens: the tile-th token that is first of 8 of its adapter ---------
+  int32_t id = -1;
+  if (tid < p.m) {
     bool bad;
-    ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
-    __syncthreads();
-  } else {
-    int32_t id = -1;
-    if (tid < p.m) {
-      bool bad;
-      id = lora_adapter(p, tid, bad);
-      if (bad && blockIdx.x == 0) flag_bad_index(p.status);
-    }
-    ids[tid] = id;
-    if (tid == 0) head[0] = -1;
-    __syncthreads();
-    // how many tokens of the same adapter come before this one
-    int before = 0;
-    if (tid < p.m) {
-      const int4* v = reinterpret_cast<const int4*>(ids);
-      for (int s = 0; s < tid; s += 4) {
-        const int4 o = v[s >> 2];
-        before += (o.x == id) + (s + 1 < tid && o.y == id) + (s + 2 < tid && o.z == id) + (s + 3 < tid && o.w == id);
-      }
-    }
-    const bool lead = tid < p.m && before % kLoraTile == 0;
-    const uint32_t leads = __ballot_sync(0xffffffffu, lead);
-    if (lane == 0) lead_count[warp] = __popc(leads);
-    __syncthreads();
-    int mine = __popc(leads & ((1u << lane) - 1)), total = 0;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) mine += lead_count[w];
-      total += lead_count[w];
-    }
-    if (tile >= total) return;  // the whole cluster
-    if (lead && mine == tile) {
-      head[0] = id;
-      head[1] = before;
-      head[2] = 0;
-    }
-    __syncthreads();
-    ad = head[0];
-    const int first = head[1];
-    const bool in = tid < p.m && id == ad && before >= first && before < first + kLoraTile;
-    if (in) tok[before - first] = tid;
-    cnt = __syncthreads_count(in);
+    id = lora_adapter(p, tid, bad);
+    if (bad && blockIdx.x == 0) flag_bad_index(p.status);
   }
+  ids[tid] = id;
+  __syncthreads();
+  int before = 0;  // tokens of the same adapter before this one
+  if (tid < p.m) {
+    const int4* v = reinterpret_cast<const int4*>(ids);
+    for (int s = 0; s < tid; s += 4) {
+      const int4 o = v[s >> 2];
+      before += (o.x == id) + (s + 1 < tid && o.y == id) + (s + 2 < tid && o.z == id) + (s + 3 < tid && o.w == id);
+    }
+  }
+  const bool lead = tid < p.m && before % COLS == 0;
+  const uint32_t leads = __ballot_sync(0xffffffffu, lead);
+  if (lane == 0) lead_count[warp] = __popc(leads);
+  __syncthreads();
+  int mine = __popc(leads & ((1u << lane) - 1)), tiles = 0;
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) mine += lead_count[w];
+    tiles += lead_count[w];
+  }
+  if (tile >= tiles) return;  // the whole cluster
+  if (lead && mine == tile) {
+    head[0] = id;
+    head[1] = before;
+  }
+  __syncthreads();
+  const int32_t ad = head[0];
+  const bool in = tid < p.m && id == ad && before >= head[1] && before < head[1] + COLS;
+  if (in) tok[before - head[1]] = tid;
+  const int cnt = __syncthreads_count(in);
 
   if (ad < 0) {  // no adapter: y as it is
-    if (warp == 0) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     if (p.out != p.y)
       for (int c = 0; c < cnt; ++c) {
         const float* src = p.y + tok[c] * p.y_stride;
         float* dst = p.out + tok[c] * p.out_stride;
-        if (VEC) {
-          const int quads = p.n >> 2;
-          for (int i = part * LORA_THREADS + tid; i < quads; i += LORA_CLUSTER * LORA_THREADS)
-            reinterpret_cast<float4*>(dst)[i] = reinterpret_cast<const float4*>(src)[i];
-          for (int i = quads * 4 + part * LORA_THREADS + tid; i < p.n; i += LORA_CLUSTER * LORA_THREADS) dst[i] = src[i];
-        } else {
-          for (int i = part * LORA_THREADS + tid; i < p.n; i += LORA_CLUSTER * LORA_THREADS) dst[i] = src[i];
-        }
+        const int quads = VEC ? p.n >> 2 : 0;
+        for (int i = part * LORA_THREADS + tid; i < quads; i += LORA_CLUSTER * LORA_THREADS)
+          reinterpret_cast<float4*>(dst)[i] = reinterpret_cast<const float4*>(src)[i];
+        for (int i = quads * 4 + part * LORA_THREADS + tid; i < p.n; i += LORA_CLUSTER * LORA_THREADS) dst[i] = src[i];
       }
     return;
   }
 
-  const bool wide = cnt > 8;  // step 3 on the tcgen05 tensor cores
-  // every block gives up its right to allocate tensor memory at once: until it
-  // does, no second block of this kernel starts on its SM (64 tokens of 24
-  // adapters: 34 us with one block per SM at a time, 20 us with two)
-  if (!wide && warp == 0) asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-  if (wide) {
-    if (warp == 0) {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(64u));
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    }
-    if (tid == 32) {
-      mbar_init(smem_u32(sm.bar), 1);
-      mbar_init(smem_u32(sm.bar) + 8, 1);
-      asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-    }
-    if (tid >= 64 && tid < 64 + cnt) {
-      sm.yoff[tid - 64] = tok[tid - 64] * p.y_stride;
-      sm.ooff[tid - 64] = tok[tid - 64] * p.out_stride;
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-  }
-  // only now: the next kernel may take tensor memory before it waits for this one
-  pdl_launch_dependents();
-
   // ---- 1. h = A x over this block's share of k -----------------------------------
-  const int rts = (p.rank + 15) >> 4;         // 16-row tiles of A
-  const int kparts = WARPS / rts;             // warps that share a tile's k
+  const int rts = (p.rank + 15) >> 4;  // 16-row tiles of A
+  const int kparts = WARPS / rts;      // warps that share a tile's k
   const int rt = warp / kparts, kp = warp - rt * kparts;
   if (rt < rts) {
     const int pieces = p.k >> 5, shares = LORA_CLUSTER * kparts, s = part * kparts + kp;
     const int g0 = (int)((int64_t)pieces * s / shares), g1 = (int)((int64_t)pieces * (s + 1) / shares);
-    float* to = sm.warp + warp * 16 * kLoraTile;
-    if (cnt <= 8)
-      lora_shrink<BF16, 1>(p, ad, rt, tok, cnt, g0, g1, to);
-    else if (cnt <= 16)
-      lora_shrink<BF16, 2>(p, ad, rt, tok, cnt, g0, g1, to);
-    else
-      lora_shrink<BF16, 4>(p, ad, rt, tok, cnt, g0, g1, to);
+    lora_shrink<BF16, 1>(p, ad, rt, tok, cnt, g0, g1, hp + warp * 16 * COLS);
   }
   __syncthreads();
-  const int cols = cnt <= 8 ? 8 : (cnt <= 16 ? 16 : 32), cshift = cnt <= 8 ? 3 : (cnt <= 16 ? 4 : 5);
-  const int entries = p.rank << cshift;
-  for (int i = tid; i < entries; i += LORA_THREADS) {
-    const int r = i >> cshift, c = i & (cols - 1);
-    const float* src = sm.warp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * kLoraTile + c;
+  for (int i = tid; i < p.rank * COLS; i += LORA_THREADS) {
+    const float* src = hp + (i / (16 * COLS)) * kparts * 16 * COLS + i % (16 * COLS);
     float s = 0.f;
-    for (int w = 0; w < kparts; ++w) s += src[w * 16 * kLoraTile];
-    sm.h[i] = s;
+    for (int w = 0; w < kparts; ++w) s += src[w * 16 * COLS];
+    h[i] = s;
   }
   cluster.sync();
 
   // ---- 2. the cluster's sum, as terms of the operand type --------------------------
-  // few entries: every block adds up all of them; more: each adds up an eighth
-  // and sends it to all
-  {
-    const bool all = entries <= 512;
-    const int quads = entries >> 2, i0 = all ? 0 : quads * part / LORA_CLUSTER;
-    const int i1 = all ? quads : quads * (part + 1) / LORA_CLUSTER;
-    for (int i = i0 + tid; i < i1; i += LORA_THREADS) {
-      float4 v[LORA_CLUSTER];
+  for (int i = tid; i < p.rank * COLS / 4; i += LORA_THREADS) {
+    float4 v[LORA_CLUSTER];
 #pragma unroll
-      for (int b = 0; b < LORA_CLUSTER; ++b) v[b] = reinterpret_cast<const float4*>(cluster.map_shared_rank(sm.h, b))[i];
+    for (int b = 0; b < LORA_CLUSTER; ++b) v[b] = reinterpret_cast<const float4*>(cluster.map_shared_rank(h, b))[i];
 #pragma unroll
-      for (int b = 1; b < LORA_CLUSTER; ++b) v[0].x += v[b].x, v[0].y += v[b].y, v[0].z += v[b].z, v[0].w += v[b].w;
-      if (all) {
-        reinterpret_cast<float4*>(sm.total)[i] = v[0];
-      } else {
-#pragma unroll
-        for (int b = 0; b < LORA_CLUSTER; ++b) reinterpret_cast<float4*>(cluster.map_shared_rank(sm.total, b))[i] = v[0];
-      }
-    }
-    if (all)
-      __syncthreads();
-    else
-      cluster.sync();
+    for (int b = 1; b < LORA_CLUSTER; ++b) v[0].x += v[b].x, v[0].y += v[b].y, v[0].z += v[b].z, v[0].w += v[b].w;
+    reinterpret_cast<float4*>(total)[i] = v[0];
   }
-  // one warp per token: lane l has ranks l, l + 32, ...
-  const float sa = p.scale ? p.scale[ad] : 1.f;
-  const int ranks = rts * 16;  // the last tile's missing ranks are zero terms
-  // (with more than 8 tokens the operand tile's 32 rows, all of them)
-  for (int c = warp; c < (wide ? kLoraTile : 8); c += WARPS) {
+  __syncthreads();
+  {
+    const int c = warp;  // a warp per token
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int r = j * 32 + lane;
-      v[j] = r < p.rank && c < cnt ? sm.total[(r << cshift) + c] : 0.f;
+      v[j] = r < p.rank && c < cnt ? total[r * COLS + c] : 0.f;
     }
-    float up = 1.f;  // what the scaled terms are multiplied by
-    if constexpr (!BF16) {
-      float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      // the largest element goes to [2^9, 2^10)
-      const int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;
-      if (e > -110 && e < 120) {
-        up = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
-        const float down = __uint_as_float((uint32_t)(9 - e + 127) << 23);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] *= down;
-      }
-    }
-    if (lane == 0) sm.mul[c] = sa * up;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = j * 32 + lane;
-      if (r >= ranks) continue;
-      float rest = v[j];
-#pragma unroll
-      for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
-        const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
-        if (!wide)
-          sm.planes[(term * 8 + c) * LoraSmem::PSTRIDE + r] = t;
-        else
-          *reinterpret_cast<uint16_t*>(sm.terms[term] + (r >> 6) * LoraSmem::PANEL_H + c * 128 +
-                                       ((((r >> 3) & 7) ^ (c & 7)) << 4) + (r & 7) * 2) = t;
-        const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
-        rest = fabsf(back) < INFINITY ? rest - back : 0.f;
-      }
-    }
+    const float up = lora_terms<BF16>(v, rts * 16, [&](int term, int r, uint16_t t) { planes[(term * COLS + c) * PSTRIDE + r] = t; });
+    if (lane == 0) mul[c] = up * (p.scale ? p.scale[ad] : 1.f);
   }
-  // before copies of y take the place of the sums, and before a block leaves,
-  // the others have read its h (those who got the sums sent have already)
-  if (entries <= 512)
-    cluster.sync();
-  else
-    __syncthreads();
+  __syncthreads();
 
   // ---- 3. out = y + s B h over this block's share of n -------------------------------
-  if (!wide) {
-    const int groups = (p.n + 31) >> 5;
-    const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER) + warp;
-    const int e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
-    lora_expand8<BF16, VEC>(p, ad, e0, e1, WARPS, tok, cnt, sm.planes, LoraSmem::PSTRIDE, sm.mul);
-    return;
+  const int groups = (p.n + 31) >> 5;
+  const int e0 = (int)((int64_t)groups * part / LORA_CLUSTER) + warp;
+  const int e1 = (int)((int64_t)groups * (part + 1) / LORA_CLUSTER);
+  lora_expand8<BF16, VEC>(p, ad, e0, e1, WARPS, tok, cnt, planes, PSTRIDE, mul);
+  cluster.sync();  // the other blocks have read this one's h
+}
+
+// ---- more than kLoraInBlock tokens -------------------------------------------------
+
+// h of the plan's tiles, split over k.  Blocks take (tile, split) in turn; the
+// warps of a block split the piece of k (and the 16-row tiles of A), so that x
+// comes from memory once and A once per 32 tokens.
+template <bool BF16>
+__global__ void __launch_bounds__(LORA_THREADS, 2) lora_shrink_kernel(const __grid_constant__ LoraParams p) {
+  constexpr int WARPS = LORA_THREADS / 32;
+  __shared__ int32_t tok[kLoraTile];
+  __shared__ __align__(16) float hp[WARPS * 16 * kLoraTile];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int units = p.plan[0] * p.splits;
+  const int rts = (p.rank + 15) >> 4, kparts = WARPS / rts;
+  const int rt = warp / kparts, kp = warp - rt * kparts;
+  for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    const int tile = u / p.splits, split = u - tile * p.splits;
+    const int i0 = p.plan[kPlanFirst + tile], cnt = p.plan[kPlanFirst + tile + 1] - i0;
+    bool bad;
+    const int32_t ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
+    if (ad < 0) continue;
+    __syncthreads();  // the previous unit's sums and tokens are read
+    if (tid < cnt) tok[tid] = p.plan[kPlanPerm + i0 + tid];
+    __syncthreads();
+    const int cols = cnt <= 8 ? 8 : (cnt <= 16 ? 16 : 32);
+    if (rt < rts) {
+      const int pieces = p.k >> 5, shares = p.splits * kparts, s = split * kparts + kp;
+      const int g0 = (int)((int64_t)pieces * s / shares), g1 = (int)((int64_t)pieces * (s + 1) / shares);
+      float* to = hp + warp * 16 * kLoraTile;
+      if (cols == 8)
+        lora_shrink<BF16, 1>(p, ad, rt, tok, cnt, g0, g1, to);
+      else if (cols == 16)
+        lora_shrink<BF16, 2>(p, ad, rt, tok, cnt, g0, g1, to);
+      else
+        lora_shrink<BF16, 4>(p, ad, rt, tok, cnt, g0, g1, to);
+    }
+    __syncthreads();
+    // out as [token][rank]: a thread has one rank
+    float* dst = p.h + ((int64_t)split * p.m + i0) * p.rank;
+    for (int i = tid; i < cnt * p.rank; i += LORA_THREADS) {
+      const int c = i / p.rank, r = i - c * p.rank;
+      const float* src = hp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * cols + c;
+      float sum = 0.f;
+      for (int w = 0; w < kparts; ++w) sum += src[w * 16 * kLoraTile];
+      dst[i] = sum;
+    }
   }
-  lora_expand32<BF16>(p, ad, cnt, part, sm);
+}
+
+// Shared memory of the second product's blocks; PANELS of 64 ranks.
+template <int PANELS>
+struct LoraSmem {
+  static constexpr int BUFS = PANELS == 1 ? 3 : 2;  // tiles of B in flight or in use
+  static constexpr int PANEL_B = 128 * 128;         // 128 features x 64 ranks
+  static constexpr int PANEL_H = kLoraTile * 128;   // 32 tokens x 64 ranks
+  uint8_t b[BUFS][PANELS * PANEL_B];
+  uint8_t terms[3][PANELS * PANEL_H];
+  float h[kLoraTile * PANELS * 64];  // the tile's A x: [token][rank]
+  // of the tokens: rows of y and out (elements), and what their sums are multiplied by
+  alignas(16) uint32_t yoff[kLoraTile];
+  alignas(16) uint32_t ooff[kLoraTile];
+  alignas(16) float mul[kLoraTile];
+  uint64_t bar[2];
+  uint32_t tmem;
+};
+
+// out = y + s B h: D [128 features][32 tokens] = B [128][rank] (terms of h)^T
+// on the tcgen05 tensor cores.  The (tile, 128 features) units, in tile order,
+// are split evenly over the blocks.  While a tile is finished (accumulator and
+// y to out) the next is multiplied and the one after it copied; its y is loaded
+// a tile ahead too.  A thread has one feature and 16 tokens, so a warp's
+// accesses of y and out are 128 bytes in a row at any alignment.
+template <bool BF16, int PANELS>
+__global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand_kernel(const __grid_constant__ LoraParams p) {
+  using S = LoraSmem<PANELS>;
+  constexpr int TERMS = BF16 ? 3 : 2, BUFS = S::BUFS;
+  constexpr uint32_t IDESC = (1u << 4) | (BF16 ? (1u << 7) | (1u << 10) : 0u) | ((kLoraTile >> 3) << 17) | ((128 >> 4) << 24);
+  constexpr int COLS = kLoraTile / 2;  // tokens of a thread
+  extern __shared__ __align__(16) uint8_t smem[];
+  S& sm = *reinterpret_cast<S*>(smem + (-smem_u32(smem) & 1023u));  // the operand tiles are aligned to 1 KB
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bar = smem_u32(sm.bar);
+
+  if (tid == 0) {
+    mbar_init(bar, 1);
+    mbar_init(bar + 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  pdl_wait();
+  // tensor memory only from here on (the kernel before may still be waiting for
+  // its own until it has ended), and the next kernel only after it (so that it
+  // cannot take this block's and then wait for it)
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "r"(64u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();
+  const uint32_t tmem = sm.tmem;
+
+  const int steps = (p.rank + 15) >> 4, fbs = (p.n + 127) >> 7;
+  const int c0 = (warp >> 2) * COLS, row = (warp & 3) * 32 + lane;
+  const int64_t units = (int64_t)p.plan[0] * fbs;
+  int64_t u = units * blockIdx.x / gridDim.x;
+  const int64_t u_end = units * (blockIdx.x + 1) / gridDim.x;
+  int it = 0;  // products issued by this block, modulo 4
+  while (u < u_end) {
+    const int tile = (int)(u / fbs), t0 = (int)(u - (int64_t)tile * fbs);
+    const int t1 = u_end - u < fbs - t0 ? t0 + (int)(u_end - u) : fbs;
+    u += t1 - t0;
+    const int i0 = p.plan[kPlanFirst + tile], cnt = p.plan[kPlanFirst + tile + 1] - i0;
+    bool bad;
+    const int32_t ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
+    if (ad < 0 && p.out == p.y) continue;
+    __syncthreads();  // the previous tile's offsets, terms and products are done with
+    if (tid < kLoraTile) {  // tokens that are not there: row 0, never written
+      const int32_t t = tid < cnt ? p.plan[kPlanPerm + i0 + tid] : 0;
+      sm.yoff[tid] = (uint32_t)t * (uint32_t)p.y_stride;
+      sm.ooff[tid] = (uint32_t)t * (uint32_t)p.out_stride;
+    }
+    if (ad < 0) {  // no adapter: y as it is
+      __syncthreads();
+      for (int t = t0; t < t1; ++t) {
+        const int f = t * 128 + row;
+        if (f >= p.n) continue;
+        float v[COLS];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) v[j] = p.y[sm.yoff[c0 + j] + f];
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+          if (c0 + j < cnt) p.out[sm.ooff[c0 + j] + f] = v[j];
+      }
+      continue;
+    }
+    // rows of 64 ranks are 128 bytes, 16-byte chunk i of row r at i ^ (r & 7)
+    // (the 128-byte swizzle); ranks up to the last step of 16 that are not
+    // there are zeros.  This thread copies chunk tid % 8 of every 32nd row.
+    const int ch = tid & 7, rw = tid >> 3;
+    const uint16_t* bsrc = static_cast<const uint16_t*>(p.b) + ((int64_t)ad * p.n + rw) * p.rank + ch * 8;
+    const uint32_t bdst = smem_u32(sm.b[0]) + rw * 128 + ((ch ^ (rw & 7)) << 4);
+    auto fetch = [&](int t, int buf) {
+      if (t < t1) {
+#pragma unroll
+        for (int pn = 0; pn < PANELS; ++pn) {
+          const int r = pn * 64 + ch * 8;
+          if (r >= steps * 16) continue;
+          const uint16_t* src = bsrc + (int64_t)t * 128 * p.rank + pn * 64;
+          const uint32_t dst = bdst + (buf * PANELS + pn) * S::PANEL_B;
+          if (t * 128 + 128 <= p.n && r < p.rank) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) cp_async16(dst + i * 32 * 128, src + i * 32 * p.rank, true);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool in = t * 128 + i * 32 + rw < p.n && r < p.rank;
+              cp_async16(dst + i * 32 * 128, in ? src + i * 32 * p.rank : static_cast<const uint16_t*>(p.b), in);
+            }
+          }
+        }
+      }
+      cp_async_commit();
+    };
+    float yv[COLS];
+    auto load_y = [&](int t) {
+      const int f = t * 128 + row;
+      if (t < t1 && f < p.n) {
+        // (tokens that are not there read row 0's y)
+#pragma unroll
+        for (int j = 0; j < COLS; j += 4) {
+          const uint4 o = *reinterpret_cast<const uint4*>(sm.yoff + c0 + j);
+          yv[j] = p.y[o.x + f], yv[j + 1] = p.y[o.y + f], yv[j + 2] = p.y[o.z + f], yv[j + 3] = p.y[o.w + f];
+        }
+      }
+    };
+    auto multiply = [&](int buf) {  // one thread
+      tc_fence_after();
+      const uint32_t d = tmem + (it & 1) * kLoraTile;
+      for (int k = 0; k < steps; ++k) {
+        const uint64_t a = umma_smem_desc(smem_u32(sm.b[buf]) + (k >> 2) * S::PANEL_B + (k & 3) * 32);
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+          umma_f16(d, a, umma_smem_desc(smem_u32(sm.terms[term]) + (k >> 2) * S::PANEL_H + (k & 3) * 32), IDESC, k + term > 0);
+      }
+      umma_commit(bar + 8 * (it & 1));
+    };
+    // the first copies run while the terms are made
+    fetch(t0, 0);
+    fetch(t0 + 1, 1);
+    for (int i = tid; i < cnt * p.rank; i += LORA_THREADS) {  // the splits' sums, eight loads in flight
+      const float* src = p.h + (int64_t)i0 * p.rank + i;
+      float v[8];
+#pragma unroll
+      for (int sp = 0; sp < 8; ++sp) v[sp] = sp < p.splits ? src[(int64_t)sp * p.m * p.rank] : 0.f;
+      sm.h[i] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    __syncthreads();
+    load_y(t0);
+    for (int c = warp; c < kLoraTile; c += LORA_THREADS / 32) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = j * 32 + lane;
+        v[j] = r < p.rank && c < cnt ? sm.h[c * p.rank + r] : 0.f;
+      }
+      const float up = lora_terms<BF16>(v, steps * 16, [&](int term, int r, uint16_t t) {
+        *reinterpret_cast<uint16_t*>(sm.terms[term] + (r >> 6) * S::PANEL_H + c * 128 + ((((r >> 3) & 7) ^ (c & 7)) << 4) +
+                                     (r & 7) * 2) = t;
+      });
+      if (lane == 0) sm.mul[c] = up * (p.scale ? p.scale[ad] : 1.f);
+    }
+    cp_async_wait<1>();
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) multiply(0);
+    int buf = 0;
+    for (int t = t0; t < t1; ++t) {
+      // here the product of tile t is under way and the copies of t + 1 are issued
+      const int nbuf = buf + 1 == BUFS ? 0 : buf + 1, fbuf = buf == 0 ? BUFS - 1 : buf - 1;
+      const uint32_t d = tmem + (it & 1) * kLoraTile, mybar = bar + 8 * (it & 1), parity = (it >> 1) & 1;
+      it = (it + 1) & 3;
+      bool good = true;
+      if constexpr (BUFS == 2) good = mbar_wait(mybar, parity, 1u << 21);  // the buffer to be filled is this product's
+      else fetch(t + BUFS - 1, fbuf);  // the buffer of tile t - 1, whose product every thread has waited for
+      if constexpr (BUFS == 3) {
+        if (t + 1 < t1) {
+          cp_async_wait<1>();
+          fence_async_smem();
+          tc_fence_before();
+          __syncthreads();
+          if (tid == 0) multiply(nbuf);
+        }
+      }
+      float v[COLS];
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) v[j] = yv[j];
+      load_y(t + 1);
+      if constexpr (BUFS == 3) good = mbar_wait(mybar, parity, 1u << 21);
+      // a wait that runs out (it cannot in a healthy launch) leaves the outputs undefined and says so
+      good = __all_sync(0xffffffffu, good);
+      if (!good && lane == 0) atomicExch(p.status, UM_TIMEOUT_STATUS);
+      if constexpr (BUFS == 2) {
+        fetch(t + 2, buf);
+        if (t + 1 < t1) {
+          cp_async_wait<1>();
+          fence_async_smem();
+          tc_fence_before();
+          __syncthreads();
+          if (tid == 0) multiply(nbuf);
+        }
+      }
+      buf = nbuf;
+      if (!good) continue;
+      tc_fence_after();
+      uint32_t acc[COLS];
+      tmem_ld16(d + ((uint32_t)((warp & 3) * 32) << 16) + c0, acc);
+      const int f = t * 128 + row;
+      if (f < p.n) {
+#pragma unroll
+        for (int j = 0; j < COLS; j += 4) {
+          const uint4 o = *reinterpret_cast<const uint4*>(sm.ooff + c0 + j);
+          const float4 m = *reinterpret_cast<const float4*>(sm.mul + c0 + j);
+          const float r0 = fmaf(__uint_as_float(acc[j]), m.x, v[j]), r1 = fmaf(__uint_as_float(acc[j + 1]), m.y, v[j + 1]);
+          const float r2 = fmaf(__uint_as_float(acc[j + 2]), m.z, v[j + 2]), r3 = fmaf(__uint_as_float(acc[j + 3]), m.w, v[j + 3]);
+          if (c0 + j + 4 <= cnt) {
+            p.out[o.x + f] = r0, p.out[o.y + f] = r1, p.out[o.z + f] = r2, p.out[o.w + f] = r3;
+          } else {
+            if (c0 + j < cnt) p.out[o.x + f] = r0;
+            if (c0 + j + 1 < cnt) p.out[o.y + f] = r1;
+            if (c0 + j + 2 < cnt) p.out[o.z + f] = r2;
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    tc_fence_before();
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(sm.tmem), "r"(64u));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(64u));
   }
 }
 

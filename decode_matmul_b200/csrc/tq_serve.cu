@@ -164,21 +164,50 @@ int check_lora(const tq_lora_t* l) {
   return TQ_OK;
 }
 
-size_t lora_ws_bytes(int32_t m) {
-  return kCounterBytes + (m > tq::kLoraInBlock ? (size_t)tq::kPlanInts * sizeof(int32_t) : 0);
+// Splits of k for more than kLoraInBlock tokens: enough (tile, split) pairs for
+// about four rounds of two blocks per SM, each of 512 features of x at least.
+int lora_splits(const tq_lora_t* l, int32_t m) {
+  const int tiles = (m + tq::kLoraTile - 1) / tq::kLoraTile;
+  int s = (4 * 2 * kAttnMaxBlocks + tiles - 1) / tiles;
+  if (s > 8) s = 8;
+  if (s > l->k / 512) s = l->k / 512;
+  return s;
 }
 
-template <bool BF16, bool VEC>
-int lora_launch(dim3 grid, const tq::LoraParams& p, cudaStream_t stream) {
-  auto kern = tq::lora_kernel<BF16, VEC>;
+constexpr size_t kLoraPlanBytes = (tq::kPlanInts * sizeof(int32_t) + 255) / 256 * 256;
+
+size_t lora_ws_bytes(const tq_lora_t* l, int32_t m) {
+  if (m <= tq::kLoraInBlock) return kCounterBytes;
+  return kCounterBytes + kLoraPlanBytes + (size_t)lora_splits(l, m) * m * l->rank * sizeof(float);
+}
+
+template <bool BF16, int PANELS>
+int lora_expand_launch(const tq::LoraParams& p, int sms, int64_t units, cudaStream_t stream) {
+  auto kern = tq::lora_expand_kernel<BF16, PANELS>;
+  constexpr size_t smem = sizeof(tq::LoraSmem<PANELS>) + 1024;
   static int configured[kMaxDevices];
   int dev = 0;
   TQ_CUDA(cudaGetDevice(&dev));
   if (!configured[dev]) {
-    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(tq::LoraSmem) + 1024));
+    TQ_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     configured[dev] = 1;
   }
-  return launch(kern, grid, dim3(tq::LORA_THREADS), sizeof(tq::LoraSmem) + 1024, stream, p);
+  int64_t grid = (int64_t)sms * (PANELS == 1 ? 3 : 2);
+  if (grid > units) grid = units;
+  return launch(kern, dim3((unsigned)grid), dim3(tq::LORA_THREADS), smem, stream, p);
+}
+
+template <bool BF16>
+int lora_prompt(const tq::LoraParams& p, int sms, int64_t tiles, cudaStream_t stream) {
+  int st = launch(tq::lora_plan_kernel, dim3(1), dim3(1024), 0, stream, p);
+  if (st != TQ_OK) return st;
+  int64_t grid = (int64_t)sms * 2;
+  if (grid > tiles * p.splits) grid = tiles * p.splits;
+  st = launch(tq::lora_shrink_kernel<BF16>, dim3((unsigned)grid), dim3(tq::LORA_THREADS), 0, stream, p);
+  if (st != TQ_OK) return st;
+  const int64_t units = tiles * ((p.n + 127) / 128);
+  return p.rank <= 64 ? lora_expand_launch<BF16, 1>(p, sms, units, stream)
+                      : lora_expand_launch<BF16, 2>(p, sms, units, stream);
 }
 
 }  // namespace
@@ -295,7 +324,7 @@ int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes) {
   int st = check_lora(lora);
   if (st != TQ_OK) return st;
   if (m < 0 || m > kMaxM) return TQ_ERR_SHAPE;
-  *bytes = lora_ws_bytes(m);
+  *bytes = lora_ws_bytes(lora, m);
   return TQ_OK;
 }
 
@@ -304,10 +333,11 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   int st = check_lora(lora);
   if (st != TQ_OK) return st;
   if (m < 0 || m > kMaxM || y_stride < lora->n || out_stride < lora->n) return TQ_ERR_SHAPE;
+  if (y_stride > (1 << 20) || out_stride > (1 << 20)) return TQ_ERR_SHAPE;  // m rows stay inside 32-bit offsets
   if (m == 0) return TQ_OK;
   if (!x_d || !adapter_d || !y_d || !out_d) return TQ_ERR_NULL;
   if (!aligned16(x_d) || !aligned_to(adapter_d, 4) || !aligned_to(y_d, 4) || !aligned_to(out_d, 4)) return TQ_ERR_ALIGN;
-  st = check_ws(workspace_d, ws_bytes, lora_ws_bytes(m));
+  st = check_ws(workspace_d, ws_bytes, lora_ws_bytes(lora, m));
   if (st != TQ_OK) return st;
   int sms = 0;
   st = check_arch(&sms);
@@ -329,18 +359,23 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   p.m = m;
   p.plan = reinterpret_cast<int32_t*>(static_cast<char*>(workspace_d) + kCounterBytes);
   p.status = status_word(workspace_d);
+  p.h = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + kCounterBytes + kLoraPlanBytes);
+  p.splits = lora_splits(lora, m);
   cudaStream_t s = (cudaStream_t)stream;
-  if (m > tq::kLoraInBlock) {
-    st = launch(tq::lora_plan_kernel, dim3(1), dim3(1024), 0, s, p);
-    if (st != TQ_OK) return st;
-  }
+  const bool bf = lora->dtype == TQ_BF16;
   // tiles: every adapter (and the tokens without one) adds at most one that is not full
-  int64_t tiles = (int64_t)(m / tq::kLoraTile) + lora->n_adapters + 1;
+  const int per = m > tq::kLoraInBlock ? tq::kLoraTile : tq::kLoraSmall;
+  int64_t tiles = (int64_t)(m / per) + lora->n_adapters + 1;
   if (tiles > m) tiles = m;
-  const dim3 grid((unsigned)tiles * tq::LORA_CLUSTER);
+  if (m > tq::kLoraInBlock)
+    return bf ? lora_prompt<true>(p, sms, tiles, s) : lora_prompt<false>(p, sms, tiles, s);
+  const dim3 grid((unsigned)tiles * tq::LORA_CLUSTER), block(tq::LORA_THREADS);
   const bool vec = aligned16(y_d) && aligned16(out_d) && y_stride % 4 == 0 && out_stride % 4 == 0;
-  if (lora->dtype == TQ_BF16) return vec ? lora_launch<true, true>(grid, p, s) : lora_launch<true, false>(grid, p, s);
-  return vec ? lora_launch<false, true>(grid, p, s) : lora_launch<false, false>(grid, p, s);
+  if (bf)
+    return vec ? launch(tq::lora_kernel<true, true>, grid, block, 0, s, p)
+               : launch(tq::lora_kernel<true, false>, grid, block, 0, s, p);
+  return vec ? launch(tq::lora_kernel<false, true>, grid, block, 0, s, p)
+             : launch(tq::lora_kernel<false, false>, grid, block, 0, s, p);
 }
 
 }  // extern "C"

@@ -488,7 +488,7 @@ typedef struct tq_lora {
  * adapter_d: device int32 [m]; an index >= n_adapters counts as no adapter and
  *   leaves TQ_ERR_VALUE in the status word.
  * y_d, out_d: device fp32, row t at t * y_stride / t * out_stride elements
- *   (>= n), 4-byte aligned (16-byte alignment and strides of a multiple of 4
+ *   (n .. 2^20), 4-byte aligned (16-byte alignment and strides of a multiple of 4
  *   are faster), so q, k or v columns of a phase's y can be addressed.  out_d
  *   may be y_d (then with the same stride); any other overlap is not allowed.
  * Products are exact, sums are fp32, and A x keeps fp32 accuracy through the

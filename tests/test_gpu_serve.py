@@ -412,6 +412,10 @@ LORA = [  # type, m, n, k, rank, adapters
     ("bf16", 600, 384, 512, 8, 2),
     ("f16", 70, 96, 17408, 40, 1),
     ("bf16", 4096, 64, 512, 16, 33),
+    ("f16", 257, 1000, 1024, 128, 3),
+    ("bf16", 700, 515, 2560, 72, 9),
+    ("bf16", 300, 129, 4608, 120, 300),
+    ("f16", 512, 2561, 1536, 24, 1),
 ]
 
 
