@@ -47,7 +47,7 @@ struct LoraParams {
   int64_t y_stride, out_stride;
   int32_t n_adapters, rank, n, k, m;
   // workspace, m > kLoraInBlock
-  int32_t* plan;    // tiles, perm [4096], first [4097]
+  int32_t* plan;    // tiles, perm [4096], of each tile (first in perm, tokens, adapter or -1, 0) [4096]
   float* h;         // [splits][m, in perm's order][rank]
   int32_t splits;   // of k
   int32_t* status;
@@ -69,7 +69,7 @@ constexpr int kLoraInBlock = 256;  // up to this many tokens each block groups t
 constexpr int kLoraSmall = 8;      // tokens of a tile up to kLoraInBlock, and beyond
 constexpr int kLoraTile = 32;
 constexpr int kLoraMaxM = 4096;
-constexpr int kPlanPerm = 4, kPlanFirst = kPlanPerm + kLoraMaxM, kPlanInts = kPlanFirst + kLoraMaxM + 4;
+constexpr int kPlanPerm = 4, kPlanTile = kPlanPerm + kLoraMaxM, kPlanInts = kPlanTile + 4 * kLoraMaxM;
 
 __device__ __forceinline__ int32_t lora_adapter(const LoraParams& p, int t, bool& bad) {
   const int32_t a = p.adapter[t];
@@ -77,15 +77,16 @@ __device__ __forceinline__ int32_t lora_adapter(const LoraParams& p, int t, bool
   return a < 0 || bad ? -1 : a;
 }
 
-// Grouping of more than kLoraInBlock tokens, by one block: a stable radix sort
-// of (adapter, token) in shared memory, five bits a pass (40 adapters: two
-// passes), then a list of where each tile begins in the sorted order.  A warp
-// takes 128 tokens in their order, 32 at a time; lanes with the same digit find
-// one another by a match, so no atomics are needed and the order is always the
-// same.
+// Grouping of more than kLoraInBlock tokens, by one block.  Tokens that come in
+// long runs of one adapter (prompts; 16 tokens a run on average) stay in their
+// order and each run makes tiles.  Others are sorted: a stable radix sort of
+// (adapter, token) in shared memory, five bits a pass (40 adapters: two
+// passes).  A warp takes 128 tokens in their order, 32 at a time; lanes with the
+// same digit find one another by a match, so no atomics are needed and the
+// order is always the same.
 __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__ LoraParams p) {
   __shared__ uint32_t key[2][kLoraMaxM];  // (adapter + 1) << 12 | token
-  __shared__ int32_t count[32][33];  // [digit][warp]
+  __shared__ int32_t count[32][33];       // [digit][warp]
   __shared__ int32_t warp_sum[32], warp_max[32];
   pdl_wait();
   pdl_launch_dependents();
@@ -101,9 +102,16 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
     }
     key[0][t] = v;
   }
+  __syncthreads();
+  int runs = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = i * 1024 + tid;
+    runs += __syncthreads_count(t < p.m && (t == 0 || (key[0][t] >> 12) != (key[0][t - 1] >> 12)));
+  }
   int cur = 0;
   const int bits = 32 - __clz(p.n_adapters + 1);  // so that the padding's bits are above all adapters'
-  for (int shift = 12; shift < 12 + bits; shift += 5) {
+  for (int shift = 12; shift < 12 + bits && runs * 16 > p.m; shift += 5) {
     count[lane][warp] = 0;
     __syncthreads();
     uint32_t v[4];
@@ -196,15 +204,18 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
     prior += __shfl_xor_sync(0xffffffffu, prior, d);
   }
   int32_t at_tile = incl - lead + prior;
+  int32_t* first = reinterpret_cast<int32_t*>(key[cur ^ 1]);  // of each tile
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i0 + i;
-    if (at < p.m && (at - start[i]) % kLoraTile == 0) p.plan[kPlanFirst + at_tile++] = at;
+    if (at < p.m && (at - start[i]) % kLoraTile == 0) first[at_tile++] = at;
   }
-  if (tid == 0) {
-    p.plan[0] = total;
-    p.plan[kPlanFirst + total] = p.m;
+  __syncthreads();
+  for (int t = tid; t < total; t += 1024) {
+    const int at = first[t], end = t + 1 < total ? first[t + 1] : p.m;
+    reinterpret_cast<int4*>(p.plan + kPlanTile)[t] = make_int4(at, end - at, (int32_t)(key[cur][at] >> 12) - 1, 0);
   }
+  if (tid == 0) p.plan[0] = total;
 }
 
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
@@ -547,9 +558,8 @@ __global__ void __launch_bounds__(LORA_THREADS, 2) lora_shrink_kernel(const __gr
   const int rt = warp / kparts, kp = warp - rt * kparts;
   for (int u = blockIdx.x; u < units; u += gridDim.x) {
     const int tile = u / p.splits, split = u - tile * p.splits;
-    const int i0 = p.plan[kPlanFirst + tile], cnt = p.plan[kPlanFirst + tile + 1] - i0;
-    bool bad;
-    const int32_t ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
+    const int4 info = reinterpret_cast<const int4*>(p.plan + kPlanTile)[tile];
+    const int i0 = info.x, cnt = info.y, ad = info.z;
     if (ad < 0) continue;
     __syncthreads();  // the previous unit's sums and tokens are read
     if (tid < cnt) tok[tid] = p.plan[kPlanPerm + i0 + tid];
@@ -642,9 +652,8 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
     const int tile = (int)(u / fbs), t0 = (int)(u - (int64_t)tile * fbs);
     const int t1 = u_end - u < fbs - t0 ? t0 + (int)(u_end - u) : fbs;
     u += t1 - t0;
-    const int i0 = p.plan[kPlanFirst + tile], cnt = p.plan[kPlanFirst + tile + 1] - i0;
-    bool bad;
-    const int32_t ad = lora_adapter(p, p.plan[kPlanPerm + i0], bad);
+    const int4 info = reinterpret_cast<const int4*>(p.plan + kPlanTile)[tile];
+    const int i0 = info.x, cnt = info.y, ad = info.z;
     if (ad < 0 && p.out == p.y) continue;
     __syncthreads();  // the previous tile's offsets, terms and products are done with
     if (tid < kLoraTile) {  // tokens that are not there: row 0, never written
@@ -706,6 +715,12 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
         }
       }
     };
+    // the lines of y three tiles ahead: to L2, so that load_y finds them there
+    auto prefetch_y = [&](int t) {
+      const int c = tid >> 2, f = t * 128 + (tid & 3) * 32;
+      if (tid < 4 * kLoraTile && t < t1 && c < cnt && f < p.n)
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.y + sm.yoff[c] + f));
+    };
     auto multiply = [&](int buf) {  // one thread
       tc_fence_after();
       const uint32_t d = tmem + (it & 1) * kLoraTile;
@@ -729,6 +744,8 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
     }
     __syncthreads();
     load_y(t0);
+    prefetch_y(t0 + 1);
+    prefetch_y(t0 + 2);
     for (int c = warp; c < kLoraTile; c += LORA_THREADS / 32) {
       float v[4];
 #pragma unroll
@@ -769,6 +786,7 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
 #pragma unroll
       for (int j = 0; j < COLS; ++j) v[j] = yv[j];
       load_y(t + 1);
+      prefetch_y(t + 3);
       if constexpr (BUFS == 3) good = mbar_wait(mybar, parity, 1u << 21);
       // a wait that runs out (it cannot in a healthy launch) leaves the outputs undefined and says so
       good = __all_sync(0xffffffffu, good);

@@ -164,14 +164,13 @@ int check_lora(const tq_lora_t* l) {
   return TQ_OK;
 }
 
-// Splits of k for more than kLoraInBlock tokens: enough (tile, split) pairs for
-// about four rounds of two blocks per SM, each of 512 features of x at least.
+// Splits of k for more than kLoraInBlock tokens: about one (tile, split) pair
+// for each of two blocks per SM, and 512 features of x for each at least.
 int lora_splits(const tq_lora_t* l, int32_t m) {
-  const int tiles = (m + tq::kLoraTile - 1) / tq::kLoraTile;
-  int s = (4 * 2 * kAttnMaxBlocks + tiles - 1) / tiles;
+  int s = 2 * kAttnMaxBlocks / ((m + tq::kLoraTile - 1) / tq::kLoraTile);
   if (s > 8) s = 8;
   if (s > l->k / 512) s = l->k / 512;
-  return s;
+  return s < 1 ? 1 : s;
 }
 
 constexpr size_t kLoraPlanBytes = (tq::kPlanInts * sizeof(int32_t) + 255) / 256 * 256;
