@@ -48,8 +48,11 @@ struct LoraParams {
   int32_t n_adapters, rank, n, k, m;
   // workspace, m > kLoraInBlock
   int32_t* plan;    // tiles, perm [4096], of each tile (first in perm, tokens, adapter or -1, 0) [4096]
-  float* h;         // [splits][m, in perm's order][rank]
+  float* h;         // of each split, in perm's order: A x of each tile as [rank][its tokens]
+  uint16_t* terms;  // in perm's order: [m][3][rank], A x as terms of the operand type
+  float* mul;       // in perm's order: what the token's sums are multiplied by
   int32_t splits;   // of k
+  int32_t* counters;
   int32_t* status;
 };
 
@@ -544,15 +547,17 @@ __global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THRE
 
 // h of the plan's tiles, split over k.  Blocks take (tile, split) in turn; the
 // warps of a block split the piece of k (and the 16-row tiles of A), so that x
-// comes from memory once and A once per 32 tokens.
+// comes from memory once and A once per 32 tokens.  The last split of a tile to
+// arrive adds all of them, in their order, and leaves the operand terms.
 template <bool BF16>
 __global__ void __launch_bounds__(LORA_THREADS, 2) lora_shrink_kernel(const __grid_constant__ LoraParams p) {
-  constexpr int WARPS = LORA_THREADS / 32;
-  __shared__ int32_t tok[kLoraTile];
+  constexpr int WARPS = LORA_THREADS / 32, TERMS = BF16 ? 3 : 2;
+  __shared__ int32_t tok[kLoraTile], last;
   __shared__ __align__(16) float hp[WARPS * 16 * kLoraTile];
+  __shared__ float h[kLoraTile * 129];  // [token][rank], odd stride
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int units = p.plan[0] * p.splits;
   const int rts = (p.rank + 15) >> 4, kparts = WARPS / rts;
   const int rt = warp / kparts, kp = warp - rt * kparts;
@@ -577,15 +582,51 @@ __global__ void __launch_bounds__(LORA_THREADS, 2) lora_shrink_kernel(const __gr
         lora_shrink<BF16, 4>(p, ad, rt, tok, cnt, g0, g1, to);
     }
     __syncthreads();
-    // out as [token][rank]: a thread has one rank
-    float* dst = p.h + ((int64_t)split * p.m + i0) * p.rank;
-    for (int i = tid; i < cnt * p.rank; i += LORA_THREADS) {
-      const int c = i / p.rank, r = i - c * p.rank;
-      const float* src = hp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * cols + c;
-      float sum = 0.f;
-      for (int w = 0; w < kparts; ++w) sum += src[w * 16 * kLoraTile];
-      dst[i] = sum;
+    // lanes are tokens, warps ranks
+    float* part = p.h + (int64_t)i0 * p.rank;
+    const int64_t step = (int64_t)p.m * p.rank;  // between splits
+    if (lane < cnt) {
+#pragma unroll 4
+      for (int r = warp; r < p.rank; r += WARPS) {
+        const float* src = hp + (r >> 4) * kparts * 16 * kLoraTile + (r & 15) * cols + lane;
+        float sum = 0.f;
+        for (int w = 0; w < kparts; ++w) sum += src[w * 16 * kLoraTile];
+        if (p.splits == 1)
+          h[lane * 129 + r] = sum;
+        else
+          part[split * step + r * cnt + lane] = sum;
+      }
     }
+    if (p.splits > 1) {
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        last = atomicAdd(p.counters + tile, 1) == p.splits - 1;
+        if (last) p.counters[tile] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (!last) continue;
+      if (lane < cnt) {
+#pragma unroll 2
+        for (int r = warp; r < p.rank; r += WARPS) {
+          float v[8];
+#pragma unroll
+          for (int sp = 0; sp < 8; ++sp) v[sp] = sp < p.splits ? __ldcg(part + sp * step + r * cnt + lane) : 0.f;
+          h[lane * 129 + r] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        }
+      }
+    }
+    __syncthreads();
+    for (int c = warp; c < cnt; c += WARPS) {
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = j * 32 + lane < p.rank ? h[c * 129 + j * 32 + lane] : 0.f;
+      uint16_t* to = p.terms + (int64_t)(i0 + c) * 3 * p.rank;
+      const float up = lora_terms<BF16>(v, p.rank, [&](int term, int r, uint16_t t) { to[term * p.rank + r] = t; });
+      if (lane == 0) p.mul[i0 + c] = up * (p.scale ? p.scale[ad] : 1.f);
+    }
+    static_assert(TERMS <= 3, "terms");
   }
 }
 
@@ -597,7 +638,6 @@ struct LoraSmem {
   static constexpr int PANEL_H = kLoraTile * 128;   // 32 tokens x 64 ranks
   uint8_t b[BUFS][PANELS * PANEL_B];
   uint8_t terms[3][PANELS * PANEL_H];
-  float h[kLoraTile * PANELS * 64];  // the tile's A x: [token][rank]
   // of the tokens: rows of y and out (elements), and what their sums are multiplied by
   alignas(16) uint32_t yoff[kLoraTile];
   alignas(16) uint32_t ooff[kLoraTile];
@@ -732,33 +772,23 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
       }
       umma_commit(bar + 8 * (it & 1));
     };
-    // the first copies run while the terms are made
+    // the operand terms of the tokens (zeros for those that are not there), 8 ranks at a time
+    for (int i = tid; i < TERMS * kLoraTile * 8 * PANELS; i += LORA_THREADS) {
+      const int hc = i & 7, c = (i >> 3) & (kLoraTile - 1), tp = i / (8 * kLoraTile), term = tp % TERMS, pn = tp / TERMS;
+      const int r = pn * 64 + hc * 8;
+      if (r < steps * 16) {
+        const bool in = c < cnt && r < p.rank;
+        cp_async16(smem_u32(sm.terms[term]) + pn * S::PANEL_H + c * 128 + ((hc ^ (c & 7)) << 4),
+                   in ? p.terms + ((int64_t)(i0 + c) * 3 + term) * p.rank + r : p.terms, in);
+      }
+    }
+    if (tid < kLoraTile) sm.mul[tid] = tid < cnt ? p.mul[i0 + tid] : 0.f;
     fetch(t0, 0);
     fetch(t0 + 1, 1);
-    for (int i = tid; i < cnt * p.rank; i += LORA_THREADS) {  // the splits' sums, eight loads in flight
-      const float* src = p.h + (int64_t)i0 * p.rank + i;
-      float v[8];
-#pragma unroll
-      for (int sp = 0; sp < 8; ++sp) v[sp] = sp < p.splits ? src[(int64_t)sp * p.m * p.rank] : 0.f;
-      sm.h[i] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-    }
-    __syncthreads();
+    __syncthreads();  // the tokens' rows
     load_y(t0);
     prefetch_y(t0 + 1);
     prefetch_y(t0 + 2);
-    for (int c = warp; c < kLoraTile; c += LORA_THREADS / 32) {
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = j * 32 + lane;
-        v[j] = r < p.rank && c < cnt ? sm.h[c * p.rank + r] : 0.f;
-      }
-      const float up = lora_terms<BF16>(v, steps * 16, [&](int term, int r, uint16_t t) {
-        *reinterpret_cast<uint16_t*>(sm.terms[term] + (r >> 6) * S::PANEL_H + c * 128 + ((((r >> 3) & 7) ^ (c & 7)) << 4) +
-                                     (r & 7) * 2) = t;
-      });
-      if (lane == 0) sm.mul[c] = up * (p.scale ? p.scale[ad] : 1.f);
-    }
     cp_async_wait<1>();
     fence_async_smem();
     tc_fence_before();

@@ -175,9 +175,18 @@ int lora_splits(const tq_lora_t* l, int32_t m) {
 
 constexpr size_t kLoraPlanBytes = (tq::kPlanInts * sizeof(int32_t) + 255) / 256 * 256;
 
+// Workspace of more than kLoraInBlock tokens: [counters][plan][A x of each
+// split][its terms][multipliers]
+size_t lora_terms_off(const tq_lora_t* l, int32_t m) {
+  return kCounterBytes + kLoraPlanBytes + ((size_t)lora_splits(l, m) * m * l->rank * sizeof(float) + 255) / 256 * 256;
+}
+size_t lora_mul_off(const tq_lora_t* l, int32_t m) {
+  return lora_terms_off(l, m) + ((size_t)m * 3 * l->rank * sizeof(uint16_t) + 255) / 256 * 256;
+}
+
 size_t lora_ws_bytes(const tq_lora_t* l, int32_t m) {
   if (m <= tq::kLoraInBlock) return kCounterBytes;
-  return kCounterBytes + kLoraPlanBytes + (size_t)lora_splits(l, m) * m * l->rank * sizeof(float);
+  return lora_mul_off(l, m) + (size_t)m * sizeof(float);
 }
 
 template <bool BF16, int PANELS>
@@ -359,6 +368,9 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   p.plan = reinterpret_cast<int32_t*>(static_cast<char*>(workspace_d) + kCounterBytes);
   p.status = status_word(workspace_d);
   p.h = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + kCounterBytes + kLoraPlanBytes);
+  p.terms = reinterpret_cast<uint16_t*>(static_cast<char*>(workspace_d) + lora_terms_off(lora, m));
+  p.mul = reinterpret_cast<float*>(static_cast<char*>(workspace_d) + lora_mul_off(lora, m));
+  p.counters = static_cast<int32_t*>(workspace_d);
   p.splits = lora_splits(lora, m);
   cudaStream_t s = (cudaStream_t)stream;
   const bool bf = lora->dtype == TQ_BF16;
