@@ -262,8 +262,11 @@ int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t qkv_str
   p.interleaved = interleaved;
   p.status = status_word(workspace_d);
   const int units = (q_heads + 2 * cache->kv_heads) * (cache->head_dim / 16);
-  const int parts = (units + tq::AP_THREADS - 1) / tq::AP_THREADS;
-  const dim3 grid((unsigned)m, (unsigned)parts), block(tq::AP_THREADS);
+  // many tokens: whole tokens to as many blocks as run at once; few: their heads are spread over blocks
+  const int32_t at_once = sms * tq::append_blocks(cache->dtype);
+  const bool many = m >= at_once / 2;
+  const int parts = many ? 1 : (units + tq::AP_THREADS - 1) / tq::AP_THREADS;
+  const dim3 grid((unsigned)(m < at_once ? m : at_once), (unsigned)parts), block(tq::AP_THREADS);
   cudaStream_t s = (cudaStream_t)stream;
   switch (cache->dtype) {
     case TQ_F16: return launch(tq::append_kernel<tq::KV_F16>, grid, block, 0, s, p);
