@@ -333,7 +333,8 @@ def tq_layer_stack_ex(args: StackArgs, h_in, seed: int, h_out, ws, spin_limit: i
 
 
 def tq_workspace_status(ws, stream=None) -> int:
-    """The workspace's device status word (TQ_OK or TQ_ERR_TIMEOUT) once the
+    """The workspace's device status word (TQ_OK, TQ_ERR_TIMEOUT, or
+    TQ_ERR_VALUE after an index out of range in device memory) once the
     stream has reached this call (synchronises the stream)."""
     v = ctypes.c_int32()
     _ok(_lib().tq_workspace_status(_ptr(ws), ctypes.byref(v), _stream(stream)), "tq_workspace_status")

@@ -5,6 +5,9 @@
     python -m decode_matmul_b200.cases rht  --m 512 --k 9728 [--reps 10]
     python -m decode_matmul_b200.cases encode --n 4096 --k 14336 [--refits 0] [--reps 5]
     python -m decode_matmul_b200.cases ldlq --n 4096 --k 4096 [--refits 0] [--reps 3]
+    python -m decode_matmul_b200.cases append --m 64 [--dtype e4m3] [--q-heads 32 --kv-heads 8 --head-dim 128]
+    python -m decode_matmul_b200.cases attn --m 64 --keys 4096 [--dtype bf16] [--page 16]
+    python -m decode_matmul_b200.cases lora --m 64 --n 5120 --k 17408 [--rank 32 --adapters 24]
 
 Runs `reps` launches after 3 warm-up launches and prints the mean time per
 launch (CUDA events) with the algorithmic bytes or FLOPs per launch.  For the
@@ -33,7 +36,7 @@ def main(argv=None):
     import tqsynth
 
     ap = argparse.ArgumentParser()
-    ap.add_argument("op", choices=["gemv", "gemm", "rht", "encode", "ldlq"])
+    ap.add_argument("op", choices=["gemv", "gemm", "rht", "encode", "ldlq", "append", "attn", "lora"])
     ap.add_argument("--refits", type=int, default=0)
     ap.add_argument("--n", type=int, default=32768)
     ap.add_argument("--k", type=int, default=16384)
@@ -44,6 +47,14 @@ def main(argv=None):
     ap.add_argument("--graph", action="store_true",
                     help="time launches replayed from a CUDA graph (no host launch cost); with --flush, a "
                          "graph of (256 MB write + launch) minus a graph of the writes alone")
+    ap.add_argument("--keys", type=int, default=4096, help="append, attn: keys of every row")
+    ap.add_argument("--q-heads", type=int, default=32)
+    ap.add_argument("--kv-heads", type=int, default=8)
+    ap.add_argument("--head-dim", type=int, default=128)
+    ap.add_argument("--page", type=int, default=16)
+    ap.add_argument("--dtype", choices=["f16", "bf16", "e4m3"], default="bf16", help="append, attn: of the cache; lora")
+    ap.add_argument("--rank", type=int, default=16)
+    ap.add_argument("--adapters", type=int, default=8)
     a = ap.parse_args(argv)
     dev = torch.device("cuda", 0)
 
@@ -74,6 +85,40 @@ def main(argv=None):
         err = torch.empty((a.n, a.k // 256), dtype=torch.float32, device=dev)
         run = lambda: tq.tq_encode(w, cb, gain, a.refits, codes, scales, err)  # noqa: E731
         work, unit = a.n * (a.k // 256) * 64.0 * 2048, "cand"
+    elif a.op in ("append", "attn"):
+        t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[a.dtype]
+        per = -(-a.keys // a.page)
+        shape = (a.m * per, a.page, a.kv_heads, a.head_dim)
+        kv = [torch.randn(shape, device=dev, dtype=torch.float16).to(t) for _ in range(2)]
+        pages = torch.randperm(a.m * per, device=dev).int().view(a.m, per)
+        cache = tq.KvCache(kv[0], kv[1], pages)
+        pos = torch.full((a.m,), a.keys - 1, dtype=torch.int32, device=dev)
+        size, width = kv[0].element_size(), (a.q_heads + 2 * a.kv_heads) * a.head_dim
+        if a.op == "append":
+            qkv = torch.randn((a.m, width), device=dev)
+            half = a.head_dim // 2
+            freq = 10000.0 ** (-torch.arange(half, dtype=torch.float64, device=dev) / half)
+            q = torch.empty((a.m, a.q_heads, a.head_dim), dtype=cache.q_dtype, device=dev)
+            ws = tq.workspace(tq.tq_kv_append_workspace(), dev)
+            run = lambda: tq.tq_kv_append(cache, qkv, a.q_heads, pos, freq, q_out=q, ws=ws)  # noqa: E731
+            work = a.m * (width * 4 + a.q_heads * a.head_dim * 2 + 2 * a.kv_heads * a.head_dim * size)
+        else:
+            q = torch.randn((a.m, a.q_heads, a.head_dim), device=dev).to(cache.q_dtype)
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            ws = tq.workspace(tq.tq_attn_workspace(cache, a.m, a.q_heads), dev)
+            run = lambda: tq.tq_attn(cache, q, pos, a.head_dim ** -0.5, out=out, ws=ws)  # noqa: E731
+            work = a.m * (a.keys * 2 * a.kv_heads * a.head_dim * size + 4 * a.q_heads * a.head_dim)
+        unit = "B"
+    elif a.op == "lora":
+        t = torch.float16 if a.dtype == "f16" else torch.bfloat16
+        la = (torch.randn((a.adapters, a.rank, a.k), device=dev) * a.k ** -0.5).to(t)
+        lora = tq.Lora(la, torch.randn((a.adapters, a.n, a.rank), device=dev).to(t))
+        x, y = torch.randn((a.m, a.k), device=dev).to(t), torch.randn((a.m, a.n), device=dev)
+        ids = torch.arange(a.m, device=dev).remainder(a.adapters).int()
+        ws = tq.workspace(tq.tq_lora_workspace(lora, a.m), dev)
+        out = torch.empty_like(y)
+        run = lambda: tq.tq_lora(lora, x, ids, y, out=out, ws=ws)  # noqa: E731
+        work, unit = min(a.adapters, a.m) * a.rank * (a.k + a.n) * 2 + a.m * (a.k * 2 + a.n * 8), "B"
     elif a.op == "rht":
         x = torch.from_numpy(tqsynth.activations(0, a.m, a.k).view(np.int16)).to(dev)
         out = torch.empty((a.m, a.k), dtype=torch.float16, device=dev)
@@ -139,7 +184,9 @@ def main(argv=None):
         ms = e0.elapsed_time(e1) / a.reps
     rate = work / (ms * 1e-3)
     how = (" (graph" + (", L2 flushed" if a.flush else "") + ")") if a.graph else (" (L2 flushed, median)" if a.flush else "")
-    print(f"{a.op} n={a.n} k={a.k} m={a.m}{how}: {ms * 1e3:.2f} us/launch, "
+    size = f"keys={a.keys} heads={a.q_heads}/{a.kv_heads}x{a.head_dim} {a.dtype}" if a.op in ("append", "attn") else (
+        f"n={a.n} k={a.k}" + (f" rank={a.rank} adapters={a.adapters}" if a.op == "lora" else ""))
+    print(f"{a.op} {size} m={a.m}{how}: {ms * 1e3:.2f} us/launch, "
           f"{rate / 1e9:.1f} G{unit}/s ({work:.4g} {unit} per launch)")
     if a.op == "ldlq":
         # the same matrix without feedback, to split the time, and the proxy loss

@@ -255,11 +255,16 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
     const int c = nt * 8 + g;
     xp[nt] = static_cast<const uint16_t*>(p.x) + (int64_t)tok[c < cnt ? c : 0] * p.k + q * 8;
   }
-  float acc[NT][4];
+  // The tensor core drops the bits below its accumulator's last place, so a
+  // long chain of MMAs drifts (17408 features in one: 2.5e-6 of the result).
+  // Every FLUSH rounds (16 to 24 MMAs) it is added to a sum of its own.
+  constexpr int FLUSH = NT == 4 ? 4 : (NT == 2 ? 2 : 1);
+  float acc[NT][4], sum[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+    for (int i = 0; i < 4; ++i) acc[nt][i] = sum[nt][i] = 0.f;
+  int round = 0;
   constexpr int U = NT == 4 ? 3 : (NT == 2 ? 4 : 8);  // pieces of 32 features in flight together
   for (int gi = g0; gi < g1; gi += U) {
     uint4 a[U][2], x[U][NT];
@@ -283,12 +288,22 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
         mma16<BF16>(acc[nt], f1, x[u][nt].z, x[u][nt].w);
       }
     }
+    if (++round == FLUSH || gi + U >= g1) {
+      round = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[nt][i] += acc[nt][i];
+          acc[nt][i] = 0.f;
+        }
+    }
   }
   // [rank in tile][token]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    *reinterpret_cast<float2*>(hp + g * NT * 8 + nt * 8 + q * 2) = make_float2(acc[nt][0], acc[nt][1]);
-    *reinterpret_cast<float2*>(hp + (g + 8) * NT * 8 + nt * 8 + q * 2) = make_float2(acc[nt][2], acc[nt][3]);
+    *reinterpret_cast<float2*>(hp + g * NT * 8 + nt * 8 + q * 2) = make_float2(sum[nt][0], sum[nt][1]);
+    *reinterpret_cast<float2*>(hp + (g + 8) * NT * 8 + nt * 8 + q * 2) = make_float2(sum[nt][2], sum[nt][3]);
   }
 }
 

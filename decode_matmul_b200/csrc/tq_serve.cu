@@ -71,7 +71,7 @@ int check_ws(const void* ws, size_t have, size_t need) {
 
 // Attention: one block per SM; two partial results per block.
 constexpr int kAttnMaxBlocks = 148;
-constexpr int kAttnMinUnits = 12;  // tiles (and item costs) a block takes before another is used
+constexpr int kAttnMinUnits = 6;   // tiles (and item costs) a block takes before another is used
 
 int attn_cols(const tq_kv_cache_t* c, int32_t q_heads) { return q_heads / c->kv_heads <= 8 ? 8 : 16; }
 

@@ -210,11 +210,15 @@ TQ_API int tq_workspace_init(void* workspace_d, size_t bytes, void* stream);
  * No call of this library clears it except tq_workspace_init, and after a
  * timeout the counter region may hold non-zero counts, so re-initialise the
  * workspace (tq_workspace_init) before using it again.
+ * The calls that read indices from device memory (tq_kv_append, tq_attn,
+ * tq_lora) write TQ_ERR_VALUE there when one is out of range; what the call
+ * does instead is said with it, and the workspace stays usable.
  * The batch-1 GEMV (tq_gemv, tq_gemv_noalloc) has no device-side wait (its
  * split tiles are summed by the last block to arrive), so it never sets it. */
 #define TQ_STATUS_OFFSET 65532
 
-/* Copy the status word of `workspace_d` to *status (TQ_OK or TQ_ERR_TIMEOUT)
+/* Copy the status word of `workspace_d` to *status (TQ_OK, TQ_ERR_TIMEOUT or
+ * TQ_ERR_VALUE)
  * after everything enqueued on `stream` before it.  The one call of this
  * library that synchronises: it waits for `stream`.  Does not clear the word. */
 TQ_API int tq_workspace_status(const void* workspace_d, int32_t* status, void* stream);

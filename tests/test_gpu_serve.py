@@ -324,6 +324,34 @@ def test_attention(kind, d, hq, hk, page, lens, window, order, out_t):
     assert torch.equal(_bytes(out), _bytes(again))
 
 
+@pytest.mark.parametrize("kind,d,hq,hk,lens", [
+    ("e4m3", 128, 8, 8, [40000, 39001, 17, 0]),   # neighbouring heads of 128 bytes: pairs of warps
+    ("e4m3", 64, 8, 8, [50001, 31999]),           # of 64 bytes: four warps
+    ("f16", 64, 24, 1, [30011, 30000, 29000]),    # 24 query heads on one key head, two groups of them
+    ("e4m3", 96, 10, 5, [33333, 33334, 33335]),   # an odd number of heads: no teams
+    ("bf16", 256, 16, 2, [9000, 3]),
+])
+def test_attention_long_rows(kind, d, hq, hk, lens):
+    """Enough keys that warps work in teams on neighbouring heads, and that rows are joined from many blocks."""
+    tq = _tq()
+    c = Case(d + len(lens), kind, d, hq, hk, 64, lens)
+    q = c.queries(9)
+    ws = tq.workspace(tq.tq_attn_workspace(c.cache, c.m, hq))
+    out = tq.tq_attn(c.cache, q, c.pos_d, d ** -0.5, c.seq_d, ws=ws)
+    c.check_attn(q, out, d ** -0.5)
+    assert (ws[:65536] == 0).all()
+    assert torch.equal(_bytes(out), _bytes(tq.tq_attn(c.cache, q, c.pos_d, d ** -0.5, c.seq_d, ws=ws)))
+
+
+def test_attention_one_row_over_the_whole_gpu():
+    """One key head: every block holds a part of the one item, joined in two rounds."""
+    tq = _tq()
+    for kind, d, hq in (("bf16", 128, 7), ("e4m3", 256, 16)):
+        c = Case(2, kind, d, hq, 1, 128, [70001])
+        q = c.queries(1)
+        c.check_attn(q, tq.tq_attn(c.cache, q, c.pos_d, d ** -0.5, c.seq_d), d ** -0.5)
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16", "e4m3"])
 def test_attention_sharp_and_flat_weights(kind):
     """Large scores of both signs (one key takes all, and keys whose weight underflows), zero and negative scales."""
@@ -460,11 +488,34 @@ def test_lora(kind, m, n, k, rank, na):
     _check_lora(x, a, b, s, runs, y, o2)
 
 
+def test_lora_runs_shorter_than_a_tile():
+    """Prompts of 17 tokens that take two adapters in turn stay in their order (more tiles than sorted tokens would
+    make); single tokens of many adapters are sorted."""
+    tq = _tq()
+    x, a, b, s, ids, y = _lora_inputs("bf16", 600, 300, 512, 16, 2)
+    for ids in (torch.arange(600).div(17, rounding_mode="floor").remainder(3).int() - 1, torch.arange(600).remainder(2).int()):
+        _check_lora(x, a, b, s, ids, y, tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y)))
+
+
+def test_lora_not_finite_tokens_stay_alone():
+    """A token with an infinite or NaN input changes no other token, in small and large tiles."""
+    tq = _tq()
+    for kind, m in (("bf16", 20), ("f16", 300)):
+        x, a, b, s, ids, y = _lora_inputs(kind, m, 200, 512, 16, 2)
+        ids[:] = 1
+        clean = tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y))
+        x[3, 7], x[m - 1, 100] = float("inf"), float("nan")
+        dirty = tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y))
+        keep = [i for i in range(m) if i not in (3, m - 1)]
+        assert torch.equal(clean[keep], dirty[keep])
+        assert not torch.isfinite(dirty[3]).any() and dirty[m - 1].isnan().all()
+
+
 def test_lora_columns_of_a_wider_output_and_no_scales():
     tq = _tq()
-    for col, width in ((0, 200), (4, 200), (3, 201), (101, 203)):
-        x, a, b, _, ids, _ = _lora_inputs("bf16", 21, 96, 512, 16, 3)
-        wide = torch.randn((21, width)).cuda()
+    for m, col, width in ((21, 0, 200), (21, 4, 200), (21, 3, 201), (21, 101, 203), (290, 3, 201)):
+        x, a, b, _, ids, _ = _lora_inputs("bf16", m, 96, 512, 16, 3)
+        wide = torch.randn((m, width)).cuda()
         keep = wide.clone()
         y = wide[:, col:col + 96]
         tq.tq_lora(tq.Lora(a, b), x, ids.cuda(), y)
@@ -508,7 +559,9 @@ def test_graphs_that_share_a_workspace_and_other_streams():
     c = Case(3, "bf16", 128, 8, 2, 16, [200, 33, 1])
     lx, la, lb, ls, lids, ly = _lora_inputs("bf16", 20, 300, 1024, 16, 4)
     lora, ids = tq.Lora(la, lb, ls), lids.cuda()
-    ws = tq.workspace(max(tq.tq_attn_workspace(c.cache, 3, 8), tq.tq_lora_workspace(lora, 20)))
+    px, _, _, _, pids, py = _lora_inputs("bf16", 320, 300, 1024, 16, 4)
+    pids_d, po = pids.cuda(), torch.empty_like(py)
+    ws = tq.workspace(max(tq.tq_attn_workspace(c.cache, 3, 8), tq.tq_lora_workspace(lora, 320)))
     qkv = torch.randn((3, 12 * 128)).cuda()
     freq = (10000.0 ** (-torch.arange(64, dtype=torch.float64) / 64)).cuda()
     q, out = torch.empty((3, 8, 128), dtype=torch.bfloat16).cuda(), torch.empty((3, 8, 128), dtype=torch.bfloat16).cuda()
@@ -520,6 +573,7 @@ def test_graphs_that_share_a_workspace_and_other_streams():
 
     def adapt():
         tq.tq_lora(lora, lx, ids, ly, out=lo, ws=ws)
+        tq.tq_lora(lora, px, pids_d, py, out=po, ws=ws)
 
     step()
     adapt()
@@ -533,6 +587,7 @@ def test_graphs_that_share_a_workspace_and_other_streams():
         pos = c.pos - shift
         c.pos_d.copy_(torch.from_numpy(pos))
         ids.copy_((lids + 1 + shift) % 5 - 1)
+        pids_d.copy_((pids + 1 + shift) % 5 - 1)
         g1.replay()
         g2.replay()
         torch.cuda.synchronize()
@@ -541,6 +596,7 @@ def test_graphs_that_share_a_workspace_and_other_streams():
         c.check_attn(q, out, 0.1)
         c.pos = saved
         _check_lora(lx, la, lb, ls, ids.cpu(), ly, lo)
+        _check_lora(px, la, lb, ls, pids_d.cpu(), py, po)
     c.pos_d.copy_(torch.from_numpy(c.pos))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
