@@ -8,7 +8,6 @@ raise.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -416,22 +415,19 @@ def _need(t, name: str, dtype, shape, device):
 
 def _on(device, stream):
     """Context in which the tensors' device is current, and the given stream too (so that what a call allocates
-    belongs to the stream it runs on)."""
+    belongs to the stream it runs on); None where that is so already."""
     import torch
     if device.type != "cuda":
         raise ValueError(f"a CUDA tensor is needed, got {device}")
     if stream is None:
-        return _AS_IS if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     return torch.cuda.stream(stream)  # makes the stream's device current as well
 
 
-_AS_IS = contextlib.nullcontext()
-
-
-def _workspace_ptr(ws, nbytes: int, device):
-    """Address and size of the workspace, `ws` or (None) a new one, which the caller keeps until its launch."""
+def _workspace(ws, nbytes: int, device):
+    """The workspace `ws`, checked, or (None) a new one."""
     import torch
     if ws is None:
         ws = workspace(nbytes, device)
@@ -529,14 +525,18 @@ def tq_kv_append(cache: KvCache, qkv, q_heads: int, pos, freq=None, interleaved:
         _need(freq, "freq", torch.float64, (half,), dev)
     if q_out is not None:
         _need(q_out, "q_out", cache.q_dtype, (m, q_heads, D), dev)
-    with _on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty((m, q_heads, D), dtype=cache.q_dtype, device=dev)
-        ws = _workspace_ptr(ws, 65536, dev)
-        st = _lib().tq_kv_append(cache._ref, qkv.data_ptr(), width if m == 1 else qkv.stride(0), m, q_heads, _addr(seq),
-                                 pos.data_ptr(), _addr(freq), 2 * half, 1 if interleaved else 0, q_out.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
-    _ok(st, "tq_kv_append")
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return tq_kv_append(cache, qkv, q_heads, pos, freq, interleaved, seq, q_out, ws)
+    if q_out is None:
+        q_out = torch.empty((m, q_heads, D), dtype=cache.q_dtype, device=dev)
+    ws = _workspace(ws, 65536, dev)
+    st = _lib().tq_kv_append(cache._ref, qkv.data_ptr(), width if m == 1 else qkv.stride(0), m, q_heads, _addr(seq),
+                             pos.data_ptr(), _addr(freq), 2 * half, 1 if interleaved else 0, q_out.data_ptr(),
+                             ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
+    if st:
+        raise TqError(st, "tq_kv_append")
     return q_out
 
 
@@ -565,13 +565,17 @@ def tq_attn(cache: KvCache, q, pos, scale: float, seq=None, window: int = 0, out
     if out is not None:
         out_dtype = TQ_F16 if out.dtype is torch.float16 else TQ_BF16
         _need(out, "out", torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, q.shape, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, device=dev)
-        ws = _workspace_ptr(ws, 0 if ws is not None else tq_attn_workspace(cache, m, q_heads), dev)
-        st = _lib().tq_attn(cache._ref, q.data_ptr(), m, q_heads, _addr(seq), pos.data_ptr(), scale, window,
-                            out.data_ptr(), out_dtype, ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
-    _ok(st, "tq_attn")
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return tq_attn(cache, q, pos, scale, seq, window, out, out_dtype, ws)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, device=dev)
+    ws = _workspace(ws, 0 if ws is not None else tq_attn_workspace(cache, m, q_heads), dev)
+    st = _lib().tq_attn(cache._ref, q.data_ptr(), m, q_heads, _addr(seq), pos.data_ptr(), scale, window, out.data_ptr(),
+                        out_dtype, ws.data_ptr(), ws.numel(), _raw_stream(dev.index))
+    if st:
+        raise TqError(st, "tq_attn")
     return out
 
 
@@ -593,10 +597,14 @@ def tq_lora(lora: Lora, x, adapter, y, out=None, ws=None, stream=None):
         if t.dtype is not torch.float32 or t.shape != (m, lora.n) or t.device != dev or (
                 lora.n > 1 and m > 0 and t.stride(1) != 1):
             raise ValueError(f"{name}: float32 [{m}][{lora.n}] with contiguous rows on {dev} is needed")
-    with _on(dev, stream):
-        ws = _workspace_ptr(ws, 0 if ws is not None else tq_lora_workspace(lora, m), dev)
-        st = _lib().tq_lora(lora._ref, x.data_ptr(), m, adapter.data_ptr(), y.data_ptr(), lora.n if m <= 1 else y.stride(0),
-                            out.data_ptr(), lora.n if m <= 1 else out.stride(0), ws.data_ptr(), ws.numel(),
-                            _raw_stream(dev.index))
-    _ok(st, "tq_lora")
+    on = _on(dev, stream)
+    if on is not None:
+        with on:
+            return tq_lora(lora, x, adapter, y, out, ws)
+    ws = _workspace(ws, 0 if ws is not None else tq_lora_workspace(lora, m), dev)
+    st = _lib().tq_lora(lora._ref, x.data_ptr(), m, adapter.data_ptr(), y.data_ptr(), lora.n if m <= 1 else y.stride(0),
+                        out.data_ptr(), lora.n if m <= 1 else out.stride(0), ws.data_ptr(), ws.numel(),
+                        _raw_stream(dev.index))
+    if st:
+        raise TqError(st, "tq_lora")
     return out
