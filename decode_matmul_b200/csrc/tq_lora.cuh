@@ -225,17 +225,20 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const __grid_constant__
 // first (64 tokens 19.6 -> 18.5 us, 4096 tokens 71 -> 67 us).  STREAM: past L1,
 // where nothing is read twice (64 tokens 17.2 us; with 32 tokens the other half
 // of each line is wanted from L1: 59 against 49 us for 4096 tokens of A x).
+// Not .nc: a block may start, and wait, while x or an adapter is still written.
 template <bool STREAM>
 __device__ __forceinline__ uint4 ldg16(const void* p) {
   uint4 v;
   if constexpr (STREAM)
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
   else
-    asm volatile("ld.global.nc.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+    asm volatile("ld.global.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "l"(p)
+                 : "memory");
   return v;
 }
 
@@ -258,14 +261,14 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
   // The tensor core drops the bits below its accumulator's last place, so a
   // long chain of MMAs drifts (17408 features in one: 2.5e-6 of the result).
   // Every FLUSH rounds (16 to 24 MMAs) it is added to a sum of its own.
-  constexpr int FLUSH = NT == 4 ? 4 : (NT == 2 ? 2 : 1);
+  constexpr int FLUSH = NT == 2 ? 2 : 4;
   float acc[NT][4], sum[NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[nt][i] = sum[nt][i] = 0.f;
   int round = 0;
-  constexpr int U = NT == 4 ? 3 : (NT == 2 ? 4 : 8);  // pieces of 32 features in flight together
+  constexpr int U = NT == 4 ? 3 : (NT == 2 ? 4 : 2);  // pieces of 32 features in flight together
   for (int gi = g0; gi < g1; gi += U) {
     uint4 a[U][2], x[U][NT];
 #pragma unroll
@@ -308,12 +311,15 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
 }
 
 // Step 3 for up to 8 tokens: this warp's groups of 32 features, e0, e0 + step,
-// ... below e1, two at a time with all their loads in flight (B 32 ranks at a
-// time, the next while these are multiplied).
+// ... below e1, GN at a time with all their loads in flight (B 32 ranks at a
+// time, the next while these are multiplied).  One at a time and two pieces of
+// A in step 1 leave registers for four blocks per SM: against two blocks with
+// twice as much in flight each, 250 tokens of 48 adapters 41 -> 30 us, 16 of 8
+// 11.2 -> 10.7, 64 of 24 16.8 -> 17.4.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, int e0, int e1, int step, const int32_t* tok,
                                              int cnt, const uint16_t* planes, int pstride, const float* mul) {
-  constexpr int GN = 2, AHEAD = 2;
+  constexpr int GN = 1, AHEAD = 2;
   constexpr int TERMS = BF16 ? 3 : 2;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
@@ -331,7 +337,7 @@ __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, in
           const bool in = on && r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            b[j][u][i] = in && f + i < p.n ? __ldg(reinterpret_cast<const uint2*>(bp + (int64_t)(f + i) * p.rank + r))
+            b[j][u][i] = in && f + i < p.n ? *reinterpret_cast<const uint2*>(bp + (int64_t)(f + i) * p.rank + r)
                                            : make_uint2(0, 0);
         }
       }
@@ -457,7 +463,7 @@ __device__ __forceinline__ float lora_terms(float v[4], int ranks, Put put) {
 }
 
 template <bool BF16, bool VEC>
-__global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 2)
+__global__ void __cluster_dims__(LORA_CLUSTER, 1, 1) __launch_bounds__(LORA_THREADS, 4)
     lora_kernel(const __grid_constant__ LoraParams p) {
   constexpr int WARPS = LORA_THREADS / 32, COLS = kLoraSmall;
   constexpr int PSTRIDE = 128 + 16;  // a token's terms, 8 words past a multiple of 32 (no bank conflicts)
