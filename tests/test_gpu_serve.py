@@ -608,6 +608,42 @@ def test_graphs_that_share_a_workspace_and_other_streams():
     _check_lora(lx, la, lb, ls, ids.cpu(), ly, l2)
 
 
+def test_adapters_between_projections():
+    """Projection, adapters, projection, adapters, launched without a pause and replayed from a graph: the projections'
+    and the prompt adapters' kernels share tensor memory and overlap their launches.  Each output is checked from the
+    inputs of its own call."""
+    import tqsynth
+    tq = _tq()
+    m, n, k = 300, 1536, 1024
+    cb = tqsynth.codebook(1)
+    hw = tqsynth.Weight(1, 0, 0, n, k, cb)
+    w = tq.DeviceWeight.from_host(hw.codes, hw.scales, torch.from_numpy(cb.view(np.int16)).cuda(), n, k)
+    x, a, b, s, ids, _ = _lora_inputs("f16", m, n, k, 16, 5)
+    lora, ids_d = tq.Lora(a, b, s), ids.cuda()
+    ys = [torch.empty((m, n)).cuda() for _ in range(6)]
+    outs = [torch.empty((m, n)).cuda() for _ in range(6)]
+    ws = tq.workspace(max(tq.tq_gemm_workspace(n, k, m), tq.tq_lora_workspace(lora, m)))
+
+    def chain():
+        for y, o in zip(ys, outs):
+            tq.tq_gemm(w, x, y, ws)
+            tq.tq_lora(lora, x, ids_d, y, out=o, ws=ws)
+
+    chain()
+    assert tq.tq_workspace_status(ws) == tq.TQ_OK
+    first = outs[0].clone()
+    _check_lora(x, a, b, s, ids, ys[0], first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain()
+    for t in ys + outs:
+        t.zero_()
+    g.replay()
+    g.replay()
+    assert tq.tq_workspace_status(ws) == tq.TQ_OK
+    assert all(torch.equal(y, ys[0]) for y in ys) and all(torch.equal(o, first) for o in outs)
+
+
 def test_empty_calls():
     tq = _tq()
     c = Case(3, "f16", 64, 4, 2, 16, [5])
