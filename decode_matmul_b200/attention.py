@@ -12,9 +12,9 @@ outputs only stand in for attention), one layer here is
     h   = phases 1, 2, 3 of a                      tq_layer_phase
 
 Every call is enqueued on the current stream and none synchronises, so a
-decode step can be captured in a CUDA graph: positions, sequences and adapters
-are read on the device, and a replay with new values in the same tensors is
-the next step.
+decode step can be captured in a CUDA graph (after `buffers`, or an earlier
+step of as many tokens): positions, sequences and adapters are read on the
+device, and a replay with new values in the same tensors is the next step.
 """
 from __future__ import annotations
 
@@ -23,7 +23,7 @@ PHASE_OPS = (("q", "k", "v"), ("o",), ("gate", "up"), ("down",))
 
 class AttentionStack:
     """layers: one dict per layer of DeviceWeights (q, k, v, o, gate, up,
-    down).  caches: one KvCache per layer (all with the same heads).  freq:
+    down), of the same sizes in every layer.  caches: one KvCache per layer (all with the same heads).  freq:
     float64 [rot/2] rotation frequencies (None: no rotation).  scale: of the
     scores (None: head_dim ** -0.5).  window: of the attention (0: all keys).
     adapters: None, or one dict per layer of Lora by op name ("q", "k", "v"),
@@ -31,19 +31,23 @@ class AttentionStack:
 
     def __init__(self, layers, caches, freq=None, interleaved: bool = False, scale=None, window: int = 0,
                  adapters=None):
-        from . import layer_struct
-        if len(caches) != len(layers) or (adapters is not None and len(adapters) != len(layers)):
+        from . import OPS, layer_struct
+        if not layers or len(caches) != len(layers) or (adapters is not None and len(adapters) != len(layers)):
             raise ValueError("one cache (and one dict of adapters) per layer is needed")
         c, w = caches[0], layers[0]
         self.q_heads, rest = divmod(w["q"].n, c.head_dim)
         if rest or self.q_heads % c.kv_heads:
             raise ValueError(f"{w['q'].n} query features do not make groups of heads of {c.head_dim}")
+        kv, hidden, inter = c.kv_heads * c.head_dim, w["q"].k, w["gate"].n
+        want = dict(q=(w["q"].n, hidden), k=(kv, hidden), v=(kv, hidden), o=(hidden, w["q"].n), gate=(inter, hidden),
+                    up=(inter, hidden), down=(hidden, inter))
         for L, cache in zip(layers, caches):
-            kv = cache.kv_heads * cache.head_dim
-            if (L["q"].n, L["k"].n, L["v"].n) != (w["q"].n, kv, kv) or cache.head_dim != c.head_dim:
-                raise ValueError("the q, k and v outputs of a layer do not match its cache's heads")
-            if L["o"].k != L["q"].n:
-                raise ValueError("the o projection's input is the q projection's width")
+            for op in OPS:
+                if (L[op].n, L[op].k) != want[op]:
+                    raise ValueError(f"{op}: {L[op].n} x {L[op].k}, but the stack's heads and first layer make it "
+                                     f"{want[op][0]} x {want[op][1]}")
+            if (cache.kv_heads, cache.head_dim, cache.q_dtype, cache.device) != (c.kv_heads, c.head_dim, c.q_dtype, c.device):
+                raise ValueError("the caches of a stack have the same heads, type of queries and device")
         for A, L in zip(adapters or (), layers):
             for op, lora in A.items():
                 if op not in PHASE_OPS[0] or (lora.n, lora.k) != (L[op].n, L[op].k):
@@ -57,11 +61,17 @@ class AttentionStack:
 
     def buffers(self, m: int) -> dict:
         """The workspace and activation buffers of steps of m tokens (kept; the last layer's values stay in them
-        after a step: y, q, attn and the phases' handoffs)."""
-        if m not in self._buf:
-            import torch
+        after a step: y, q, attn and the phases' handoffs).  All steps of m tokens share them, so those follow one
+        another on one stream.  A captured step's must exist before the capture, from an earlier step or this call:
+        what a capture clears is clear only when it is replayed."""
+        import torch
 
-            from . import tq_attn_workspace, tq_layer_phase_workspace, tq_lora_workspace, workspace
+        from . import tq_attn_workspace, tq_layer_phase_workspace, tq_lora_workspace, workspace
+        if m in self._buf:
+            return self._buf[m]
+        with torch.cuda.device(self.device):  # on whose current stream the workspace is cleared
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"buffers({m}) has to be called before a step of {m} tokens is captured")
             n = max(tq_layer_phase_workspace(s, p, m) for s in self.structs for p in range(4))
             n = max([n] + [tq_attn_workspace(c, m, self.q_heads) for c in self.caches]
                     + [tq_lora_workspace(a, m) for A in self.adapters or () for a in A.values()])
@@ -90,10 +100,12 @@ class AttentionStack:
         if self.adapters is not None and adapter is None:
             raise ValueError("adapter: int32 [m] is needed, since the stack has adapters")
         m = h.shape[0]
-        if h.dtype != torch.int16 or h.shape[1] != self.layers[0]["q"].k or not h.is_contiguous() or h.device != self.device:
+        if h.dtype != torch.int16 or h.dim() != 2 or h.shape[1] != self.layers[0]["q"].k or not h.is_contiguous() or h.device != self.device:
             raise ValueError(f"h: contiguous int16 [m][{self.layers[0]['q'].k}] on {self.device} is needed")
         if out is None:
             out = torch.empty_like(h)
+        elif out.dtype != h.dtype or out.shape != h.shape or not out.is_contiguous() or out.device != h.device:
+            raise ValueError(f"out: like h, contiguous int16 {tuple(h.shape)} on {self.device}, is needed")
         if m == 0:
             return out
         b = self.buffers(m)

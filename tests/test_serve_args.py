@@ -2,6 +2,7 @@
 refusal comes before any device call, through the C ABI with fake aligned
 addresses that nothing dereferences and through the Python binding with CPU
 tensors."""
+import contextlib
 import ctypes
 
 import numpy as np
@@ -138,6 +139,50 @@ def test_binding_refuses_wrong_tensors():
     for args in ((x.half(), ids, y), (x, ids.long(), y), (x, ids, y[:, :8]), (x, ids, y.double()), (x, ids, y)):
         with pytest.raises(ValueError):
             tq.tq_lora(lora, *args)
+
+
+def _stack_parts(dtypes=(torch.bfloat16, torch.bfloat16), heads=(2, 2), **sizes):
+    """Two layers of weights without bytes (hidden 512, 4 query and 2 key heads of 64, 1024 between) and their caches;
+    sizes: what the second layer has instead."""
+    shape = dict(q=(256, 512), k=(128, 512), v=(128, 512), o=(512, 256), gate=(1024, 512), up=(1024, 512), down=(512, 1024))
+    none = torch.zeros(0)
+    layers = [{op: tq.DeviceWeight(none, none, none, *s) for op, s in d.items()} for d in (shape, {**shape, **sizes})]
+    caches = [tq.KvCache(torch.zeros((4, 16, n, 64), dtype=t), torch.zeros((4, 16, n, 64), dtype=t),
+                         torch.zeros((2, 3), dtype=torch.int32)) for t, n in zip(dtypes, heads)]
+    return layers, caches
+
+
+def test_stack_refusals(monkeypatch):
+    """A stack whose layers would not fit its buffers, an output that is not like its input, and a capture before the
+    buffers are there."""
+    from decode_matmul_b200.attention import AttentionStack
+    layers, caches = _stack_parts()
+    stack = AttentionStack(layers, caches)
+    AttentionStack(*_stack_parts(dtypes=(torch.float16, torch.float8_e4m3fn)))
+    for bad in (dict(gate=(2048, 512), up=(2048, 512), down=(512, 2048)), dict(o=(1024, 256)), dict(down=(1024, 1024)),
+                dict(q=(512, 512), o=(512, 512)), dict(k=(256, 512), v=(256, 512), heads=(2, 4)),
+                dict(dtypes=(torch.float16, torch.bfloat16)), dict(heads=(4, 4)), dict(up=(512, 512))):
+        with pytest.raises(ValueError):
+            AttentionStack(*_stack_parts(**bad))
+    for args in ((layers, caches[:1]), ([], []), (layers, caches, None, False, None, 0, [{}])):
+        with pytest.raises(ValueError):
+            AttentionStack(*args)
+    lora = tq.Lora(torch.zeros((1, 8, 512)).bfloat16(), torch.zeros((1, 128, 8)).bfloat16())
+    with pytest.raises(ValueError):
+        AttentionStack(layers, caches, adapters=[{"q": lora}, {}])
+    h, pos = torch.zeros((2, 512), dtype=torch.int16), torch.zeros(2, dtype=torch.int32)
+    for args in ((h.float(), pos), (h[:, :256], pos), (h[0], pos), (h.t().contiguous().t(), pos)):
+        with pytest.raises(ValueError):
+            stack.forward(*args, 0)
+    for out in (h[:1], h.float(), torch.zeros((2, 1024), dtype=torch.int16)[:, :512]):
+        with pytest.raises(ValueError):
+            stack.forward(h, pos, 0, out=out)
+    with pytest.raises(ValueError):  # no adapter indices
+        AttentionStack(layers, caches, adapters=[{}, {"k": lora}]).forward(h, pos, 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    with pytest.raises(RuntimeError, match="captured"):
+        stack.buffers(2)
 
 
 def test_plain_forms():
