@@ -192,10 +192,7 @@ __global__ void __launch_bounds__(AP_THREADS, append_blocks(T)) append_kernel(Ap
       const bool is_q = head < p.q_heads;
       float x[8], y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // a padded row: a zero query
-        x[i] = pos < 0 ? 0.f : nx[i];
-        y[i] = pos < 0 ? 0.f : ny[i];
-      }
+      for (int i = 0; i < 8; ++i) x[i] = nx[i], y[i] = ny[i];
       load(t, u + ustep);
       if (!is_q && slot < 0) continue;
       if (pos < 0) {  // padded row: a zero query
