@@ -592,6 +592,13 @@ __global__ void __launch_bounds__(LORA_THREADS, 2) lora_shrink_kernel(const __gr
   __shared__ int32_t tok[kLoraTile], last;
   __shared__ __align__(16) float hp[WARPS * 16 * kLoraTile];
   __shared__ float h[kLoraTile * 129];  // [token][rank], odd stride
+  // While the tokens are still being grouped: the first 8 MB of x to L2 (what
+  // comes from memory in that time; 1000 tokens 57.6 -> 56.1 us, 4096 tokens
+  // 67.6 -> 67.0, with 24 MB 68.1).
+  const int64_t kbs = (int64_t)p.m * (p.k >> 9);  // of 512 features
+  for (int64_t c = blockIdx.x * LORA_THREADS + threadIdx.x; c < (kbs < 8192 ? kbs : 8192); c += gridDim.x * LORA_THREADS)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(static_cast<const uint8_t*>(p.x) + c * 1024),
+                 "r"(1024u));
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
