@@ -68,6 +68,7 @@ struct AttnCfg {
   static constexpr int KT = TK / 16;
   static constexpr int STAGE = 2 * TK * RB;  // the keys, then the values
   static constexpr int COLS = 8 * NT;        // head columns
+  static constexpr int TERMS = T == KV_BF16 ? 3 : 2;  // of a weight (AttnWeights)
   static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
   static constexpr int SLOT = PART * 4;
   static constexpr int CTL = 2048;
@@ -137,6 +138,37 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
   else
     mma_16816(c, a, b0, b1);
 }
+
+// The weights of the second product as MMA operands.  They are at most 2^UP and
+// the sum of two keys' terms (a pair in each word) is the binary32 weight:
+// three bf16 terms (24 bits), or two fp16 terms (22 bits).  UP = 15 for fp16:
+// its smallest step, 2^-24, then is 2^-39 of the largest weight; with weights of
+// at most 1 a key of less than 2^-25 would add nothing to O while the sum of the
+// weights still counted it (16384 keys 18 below one key in e^s: all of their
+// part of the output lost).  O and the sum carry the same 2^UP, which cancels.
+// With one fp16 term (2^-12) or two of bf16 (2^-17) 6 to 10%, or 0.2%, of the bf16
+// outputs were rounded to the other neighbour.
+template <int T>
+struct AttnWeights {
+  static constexpr bool BF = T == KV_BF16;
+  static constexpr int TERMS = BF ? 3 : 2;
+  static constexpr float UP = BF ? 0.f : 15.f;
+  static __device__ __forceinline__ void split(float a, float b, uint32_t t[TERMS]) {
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+      if constexpr (BF) {
+        t[k] = KvElem<KV_BF16>::pack2(a, b);
+        a -= __uint_as_float(t[k] << 16);
+        b -= __uint_as_float(t[k] & 0xffff0000u);
+      } else {
+        t[k] = f2_to_h2(a, b);
+        const float2 f = h2_to_f2(t[k]);
+        a -= f.x;
+        b -= f.y;
+      }
+    }
+  }
+};
 
 // The visible keys of a row.
 struct AttnRow {
@@ -716,16 +748,13 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               }
             }
         }
-        // P^T as the B operand.  fp16 weights are rounded to 2^-12 (e4m3 and
-        // fp16 caches; at most 1, exact for a key that takes all); bf16
-        // caches need bf16 weights, whose 2^-9 would be felt in the output,
-        // so they go in as two terms (2^-17) and two MMAs.
-        uint32_t ph[KT][NT][2], pl[KT][NT][2];
+        // P^T as the B operand, in terms that keep binary32 accuracy (AttnWeights)
+        uint32_t pt[C::TERMS][KT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float m0[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) m0[i] = mx[nt][i] == -INFINITY ? 0.f : -mx[nt][i] * sc;
+          for (int i = 0; i < 2; ++i) m0[i] = mx[nt][i] == -INFINITY ? 0.f : AttnWeights<T>::UP - mx[nt][i] * sc;
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -738,15 +767,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
                 e[i] = vm == FULL_MASK || x != -INFINITY ? ex2(fmaf(x, sc, m0[i])) : 0.f;
                 sum[nt][i] += e[i];
               }
-              if constexpr (BF) {
-                const uint32_t h = KvElem<KV_BF16>::pack2(e[0], e[1]);
-                const uint32_t l =
-                    KvElem<KV_BF16>::pack2(e[0] - __uint_as_float(h << 16), e[1] - __uint_as_float(h & 0xffff0000u));
-                ph[kt][nt][r] = transpose8(h);
-                pl[kt][nt][r] = transpose8(l);
-              } else {
-                ph[kt][nt][r] = transpose8(f2_to_h2(e[0], e[1]));
-              }
+              uint32_t t[C::TERMS];
+              AttnWeights<T>::split(e[0], e[1], t);
+#pragma unroll
+              for (int k = 0; k < C::TERMS; ++k) pt[k][kt][nt][r] = transpose8(t[k]);
             }
         }
         // O^T
@@ -761,10 +785,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               uint32_t a[4];
               ldsm4_t(a, va + kt * 16 * C::RB + (vx ^ (mt * 32)));
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma16<BF>(o[mt][nt], a, ph[kt][nt][0], ph[kt][nt][1]);
-                if constexpr (BF) mma16<BF>(o[mt][nt], a, pl[kt][nt][0], pl[kt][nt][1]);
-              }
+              for (int k = 0; k < C::TERMS; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt][nt], a, pt[k][kt][nt][0], pt[k][kt][nt][1]);
             }
         } else {
           // a 16-bit element of the transposed load is a pair of neighbouring
@@ -782,7 +805,9 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
                 e4m3x4_to_h2(__byte_perm(r[2 * u], 0, 0x3120), a[0], a[1]);
                 e4m3x4_to_h2(__byte_perm(r[2 * u + 1], 0, 0x3120), a[2], a[3]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, ph[kt][nt][0], ph[kt][nt][1]);
+                for (int k = 0; k < C::TERMS; ++k)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, pt[k][kt][nt][0], pt[k][kt][nt][1]);
               }
             }
         }

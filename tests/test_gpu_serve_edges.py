@@ -1,0 +1,67 @@
+"""Cache append, paged attention and adapters on the GPU where their numbers
+are hard: weak keys beside a strong one, very long rows, infinities, the same
+slot twice, and the accuracy that the kernels claim."""
+import numpy as np
+import pytest
+import torch
+
+import serve_ref as ref
+from test_gpu_serve import TYPES, Case, _num, _tq
+
+pytestmark = pytest.mark.gpu
+
+
+def _cache(kind, k, v, page=64):
+    """One sequence of the rows of k and v ([tokens][kv_heads][d]), in pages in order."""
+    shape = (k.shape[0] // page, page) + tuple(k.shape[1:])
+    k, v = (x.view(shape).to(TYPES[kind]).cuda() for x in (k, v))
+    return _tq().KvCache(k, v, torch.arange(shape[0], dtype=torch.int32, device="cuda").view(1, -1))
+
+
+def _rows(m, last):
+    """Positions and sequences of m rows that see keys 0 .. last of sequence 0."""
+    pos = torch.full((m,), last, dtype=torch.int32, device="cuda")
+    return pos, torch.zeros_like(pos)
+
+
+# ---- attention -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("gap", [16.0, 18.0, 20.0])
+def test_attention_many_weak_keys_beside_a_strong_one(kind, gap):
+    """16383 equal keys whose scores are `gap` below one key's, in as many items as there are warps, so that one warp
+    has all of a row.  The strong key's value is 0: the output is what the weak ones leave of theirs."""
+    tq = _tq()
+    n, d, hk, m = 16384, 64, 8, 148
+    k, v = torch.zeros((n, hk, d)), torch.full((n, hk, d), 32.0)
+    k[5], v[5] = gap, 0.0
+    cache = _cache(kind, k, v)
+    pos, seq = _rows(m, n - 1)
+    out = tq.tq_attn(cache, torch.ones((m, hk, d), dtype=cache.q_dtype).cuda(), pos, 1 / d, seq, out_dtype=tq.TQ_F16)
+    w = (n - 1) * np.exp(-gap)
+    want = 32.0 * w / (1.0 + w)
+    # the output's rounding (2^-11 and half of fp16's smallest step); binary32 running sums: 4096 additions of a lane
+    # at 2^-24 of the total, and their exponentials
+    bound = want * (2.0 ** -11 + 4096 * 2.0 ** -24 + 2.0 ** -20) + 2.0 ** -25
+    assert float((out.double() - want).abs().max()) <= bound
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("d,hq,hk", [(64, 8, 4), (128, 8, 2), (256, 12, 1)])
+def test_attention_weights_keep_32_bits(kind, d, hq, hk):
+    """Rows of a few keys with fp16 output: nothing but the output's rounding, the scores' binary32 sums and 2^-20 for
+    exponentials, weights and sums."""
+    tq = _tq()
+    c = Case(d, kind, d, hq, hk, 16, [int(x) for x in np.random.default_rng(d).integers(2, 90, 24)])
+    q = c.queries(5)
+    got = _num(tq.tq_attn(c.cache, q, c.pos_d, d ** -0.5, c.seq_d, out_dtype=tq.TQ_F16))
+    K, V = c.values()
+    qn, grp = _num(q), hq // hk
+    for i in range(c.m):
+        j = np.arange(int(c.pos[i]) + 1)
+        at = c.table[c.seq[i], j // c.page], j % c.page
+        for h in range(hk):
+            sl = slice(h * grp, (h + 1) * grp)
+            want, size, score = ref.attention(qn[i, sl], K[at][:, h], V[at][:, h], d ** -0.5)
+            bound = np.abs(want) * 2.0 ** -11 + size * (2 * score * (d / 16 + 8) * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -25
+            assert (np.abs(got[i, sl] - want) <= bound).all(), (i, h)
