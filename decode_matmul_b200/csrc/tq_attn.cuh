@@ -773,43 +773,52 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               for (int k = 0; k < C::TERMS; ++k) pt[k][kt][nt][r] = transpose8(t[k]);
             }
         }
-        // O^T
-        if constexpr (!F8) {
-          const int vrow = (lane & 7) + (lane >> 4) * 8;
-          const uint32_t va = vb + vrow * C::RB;
-          const uint32_t vx = (((lane >> 3) & 1) ^ C::swz(vrow)) * 16;
+        // O^T: the tile's share, two row tiles at a time, is added to O by the
+        // threads.  The tensor core drops the bits below its accumulator's last
+        // place, which in one chain over 2^20 keys made outputs 1% too small.
+        // Small terms first, so that most of them are added to small sums.
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt)
+        for (int mt = 0; mt < MT; mt += 2) {
+          float t[2][NT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint32_t a[4];
-              ldsm4_t(a, va + kt * 16 * C::RB + (vx ^ (mt * 32)));
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int k = 0; k < C::TERMS; ++k)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt][nt], a, pt[k][kt][nt][0], pt[k][kt][nt][1]);
-            }
-        } else {
-          // a 16-bit element of the transposed load is a pair of neighbouring
-          // features: MMA rows r and r + 8 are features 2r and 2r + 1
-          const uint32_t va = vb + krow * C::RB;
+              for (int i = 0; i < 4; ++i) t[u][nt][i] = 0.f;
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int mt = 0; mt < MT; mt += 2) {
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t a[2][4];
+            if constexpr (!F8) {
+              const int vrow = (lane & 7) + (lane >> 4) * 8;
+              const uint32_t va = vb + (kt * 16 + vrow) * C::RB;
+              const uint32_t vx = (((lane >> 3) & 1) ^ C::swz(vrow)) * 16;
+              ldsm4_t(a[0], va + (vx ^ (mt * 32)));
+              ldsm4_t(a[1], va + (vx ^ (mt * 32 + 32)));
+            } else {
+              // a 16-bit element of the transposed load is a pair of neighbouring
+              // features: MMA rows r and r + 8 are features 2r and 2r + 1
               uint32_t r[4];
-              ldsm4_t(r, va + kt * 16 * C::RB + (kx ^ (mt * 16)));
+              ldsm4_t(r, vb + (kt * 16 + krow) * C::RB + (kx ^ (mt * 16)));
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                uint32_t a[4];
-                e4m3x4_to_h2(__byte_perm(r[2 * u], 0, 0x3120), a[0], a[1]);
-                e4m3x4_to_h2(__byte_perm(r[2 * u + 1], 0, 0x3120), a[2], a[3]);
-#pragma unroll
-                for (int k = 0; k < C::TERMS; ++k)
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) mma16<BF>(o[mt + u][nt], a, pt[k][kt][nt][0], pt[k][kt][nt][1]);
+                e4m3x4_to_h2(__byte_perm(r[2 * u], 0, 0x3120), a[u][0], a[u][1]);
+                e4m3x4_to_h2(__byte_perm(r[2 * u + 1], 0, 0x3120), a[u][2], a[u][3]);
               }
             }
+#pragma unroll
+            for (int k = C::TERMS - 1; k >= 0; --k)
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma16<BF>(t[u][nt], a[u], pt[k][kt][nt][0], pt[k][kt][nt][1]);
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[mt + u][nt][i] += t[u][nt][i];
         }
       }
       if (++stage_out == S) stage_out = 0;

@@ -65,3 +65,19 @@ def test_attention_weights_keep_32_bits(kind, d, hq, hk):
             want, size, score = ref.attention(qn[i, sl], K[at][:, h], V[at][:, h], d ** -0.5)
             bound = np.abs(want) * 2.0 ** -11 + size * (2 * score * (d / 16 + 8) * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -25
             assert (np.abs(got[i, sl] - want) <= bound).all(), (i, h)
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_attention_sums_over_a_million_keys(kind):
+    """Equal weights over 2^20 keys, in as many items as there are warps: the output is the mean of the values."""
+    tq = _tq()
+    n, d, hk, m = 1 << 20, 64, 8, 148
+    g = torch.Generator(device="cuda").manual_seed(1)
+    v = torch.empty((n // 64, 64, hk, d), dtype=torch.float16, device="cuda").uniform_(0.5, 1.0, generator=g).to(TYPES[kind])
+    cache = tq.KvCache(torch.zeros_like(v), v, torch.arange(n // 64, dtype=torch.int32, device="cuda").view(1, -1))
+    pos, seq = _rows(m, n - 1)
+    out = tq.tq_attn(cache, torch.zeros((m, hk, d), dtype=cache.q_dtype, device="cuda"), pos, 1.0, seq, out_dtype=tq.TQ_F16)
+    want = torch.stack([v[:, :, h].double().mean((0, 1)) for h in range(hk)])
+    # the output's rounding; 2^15 or 2^16 additions of a tile's share, each rounded to nearest by at most 2^-24 with
+    # an error of either sign: 2^8 times that, four times over
+    assert float(((out.double() - want).abs() / want).max()) <= 2.0 ** -11 + 4 * 2.0 ** 8 * 2.0 ** -24
