@@ -148,25 +148,43 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
 // part of the output lost).  O and the sum carry the same 2^UP, which cancels.
 // With one fp16 term (2^-12) or two of bf16 (2^-17) 6 to 10%, or 0.2%, of the bf16
 // outputs were rounded to the other neighbour.
+// For 16-bit caches every term of a weight is positive: an infinite value then
+// gives its infinity, where a term of 0 or of the other sign would make it NaN.
+// So all terms but the last are rounded down from below what is left of the
+// weight.  fp16's are at least its smallest step, so weights below 2^-38 of the
+// largest count as that much (hidden keys too: their values are zeros).
 template <int T>
 struct AttnWeights {
-  static constexpr bool BF = T == KV_BF16;
-  static constexpr int TERMS = BF ? 3 : 2;
-  static constexpr float UP = BF ? 0.f : 15.f;
+  static constexpr int TERMS = T == KV_BF16 ? 3 : 2;
+  static constexpr float UP = T == KV_BF16 ? 0.f : 15.f;
+  static constexpr float BELOW = 0x1.fffffep-1f;  // x * BELOW < x in binary32 (by one step, or half of one)
   static __device__ __forceinline__ void split(float a, float b, uint32_t t[TERMS]) {
+    if constexpr (T == KV_BF16) {
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k) {
-      if constexpr (BF) {
-        t[k] = KvElem<KV_BF16>::pack2(a, b);
-        a -= __uint_as_float(t[k] << 16);
-        b -= __uint_as_float(t[k] & 0xffff0000u);
-      } else {
-        t[k] = f2_to_h2(a, b);
-        const float2 f = h2_to_f2(t[k]);
-        a -= f.x;
-        b -= f.y;
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t ha = __float_as_uint(a * BELOW), hb = __float_as_uint(b * BELOW);
+        t[k] = __byte_perm(ha, hb, 0x7632);
+        a -= __uint_as_float(ha & 0xffff0000u);
+        b -= __uint_as_float(hb & 0xffff0000u);
       }
+      t[2] = KvElem<KV_BF16>::pack2(a, b);
+    } else {
+      constexpr float STEP = 0x1p-24f;  // two of them are left at least where there are three, so that t[1] rounds to nearest
+      if constexpr (T == KV_F16) {
+        asm("cvt.rz.f16x2.f32 %0, %1, %2;\n" : "=r"(t[0]) : "f"(fmaf(b, BELOW, -2 * STEP)), "f"(fmaf(a, BELOW, -2 * STEP)));
+        t[0] = max_h2(t[0], 0x00010001u);
+      } else {
+        t[0] = f2_to_h2(a, b);
+      }
+      const float2 f = h2_to_f2(t[0]);
+      t[1] = f2_to_h2(a - f.x, b - f.y);
+      if constexpr (T == KV_F16) t[1] = max_h2(t[1], 0x00010001u);
     }
+  }
+  static __device__ __forceinline__ uint32_t max_h2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
   }
 };
 

@@ -451,6 +451,8 @@ TQ_API int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t 
  *   maxima, sums and outputs are fp32 until the last rounding.
  * A row that sees no key (pos_d[t] < 0: a padded row) gives zeros.  Cache
  *   bytes of positions that no row sees are not used, whatever they hold.
+ *   An infinite value that is seen gives its infinity, unless its weight
+ *   underflows fp32 beside the largest (NaN then, as 0 times infinity is).
  * A sequence or position outside the table makes its row see no key, a page
  *   index outside the cache hides that page's keys; both leave TQ_ERR_VALUE in
  *   the status word.

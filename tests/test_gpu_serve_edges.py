@@ -81,3 +81,37 @@ def test_attention_sums_over_a_million_keys(kind):
     # the output's rounding; 2^15 or 2^16 additions of a tile's share, each rounded to nearest by at most 2^-24 with
     # an error of either sign: 2^8 times that, four times over
     assert float(((out.double() - want).abs() / want).max()) <= 2.0 ** -11 + 4 * 2.0 ** 8 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("strong", [2.5, 20.0])
+def test_attention_infinite_values(kind, strong):
+    """An infinity among the visible values is the output's infinity, down to weights of e^-40 of the largest, and stays
+    in its feature and in the rows that see it.  A weight that underflows binary32 (below e^-87) makes it NaN, as 0
+    times infinity is."""
+    tq = _tq()
+    n, d, hk, hq, scale = 4096, 64, 2, 4, 0.125
+    g = torch.Generator().manual_seed(1)
+    k, v = torch.randn((n, hk, d), generator=g), torch.randn((n, hk, d), generator=g)
+    v[3, :, 7], v[100, :, 9], v[2000, 1, 11] = float("inf"), -float("inf"), float("inf")
+    q = torch.randn((8, hq, d), generator=g)
+    k[4], q[:, 1] = strong, 2.0  # query head 1: key 4 is 16 strong (40 or 320) above the rest's middle
+    cache = _cache(kind, k, v)
+    q = q.to(cache.q_dtype).cuda()
+    last = [3, 50, 200, 4095, 2, 99, 100, 2100]
+    pos = torch.tensor(last, dtype=torch.int32).cuda()
+    got = _num(tq.tq_attn(cache, q, pos, scale, torch.zeros_like(pos), out_dtype=tq.TQ_F16))
+    K, V, qn = _num(cache.k).reshape(n, hk, d), _num(cache.v).reshape(n, hk, d), _num(q)
+    for i, p in enumerate(last):
+        for h in range(hk):
+            sl = slice(2 * h, 2 * h + 2)
+            want, size, score = ref.attention(qn[i, sl], K[:p + 1, h], V[:p + 1, h], scale)
+            s = scale * (qn[i, sl] @ K[:p + 1, h].T)
+            gone = s - s.max(axis=1, keepdims=True) < -87.0
+            nan = (gone[:, :, None] & np.isinf(V[:p + 1, h])).any(axis=1)
+            inf = np.isinf(want) & ~nan
+            assert (np.isinf(got[i, sl]) | np.isnan(got[i, sl]))[nan].all(), (i, h)
+            assert np.array_equal(got[i, sl][inf], want[inf]), (i, h)
+            bound = ref.attention_bound(want, size, score, p + 1, 6.0, torch.float16, cache.k.dtype)
+            ok = ~np.isinf(want)
+            assert (np.abs(got[i, sl][ok] - want[ok]) <= bound[ok]).all(), (i, h)
