@@ -428,18 +428,22 @@ __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, in
 
 // h of one token as terms of the operand type: lane l has ranks l, l + 32, ...
 // in v; put(term, rank, bits) takes them.  Returns what the scaled terms are to
-// be multiplied by.
+// be multiplied by.  Every term of an element has its sign and, unless the
+// element is 0, is not 0 (all but the last are rounded down from below what is
+// left of its size; fp16's are at least the smallest step, 2^-33 of the largest
+// element), so that an infinite B gives its infinity, not 0 times infinity.
 template <bool BF16, class Put>
 __device__ __forceinline__ float lora_terms(float v[4], int ranks, Put put) {
   const int lane = threadIdx.x & 31;
+  constexpr float BELOW = 0x1.fffffep-1f, STEP = 0x1p-24f;  // x * BELOW < x; fp16's smallest step
   float up = 1.f;
   if constexpr (!BF16) {
     float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    // the largest element goes to [2^9, 2^10)
-    const int e = (int)((__float_as_uint(top) >> 23) & 255) - 127;
-    if (e > -110 && e < 120) {
+    // the largest element goes to [2^9, 2^10); sums of fp16 products are below 2^64 or infinite
+    const int e = min((int)((__float_as_uint(top) >> 23) & 255) - 127, 64);
+    if (e > -110) {
       up = __uint_as_float((uint32_t)(e - 9 + 127) << 23);
       const float down = __uint_as_float((uint32_t)(9 - e + 127) << 23);
 #pragma unroll
@@ -450,13 +454,26 @@ __device__ __forceinline__ float lora_terms(float v[4], int ranks, Put put) {
   for (int j = 0; j < 4; ++j) {
     const int r = j * 32 + lane;
     if (r >= ranks) continue;
-    float rest = v[j];
+    constexpr int TERMS = BF16 ? 3 : 2;
+    const uint16_t sign = (uint16_t)(__float_as_uint(v[j]) >> 16 & 0x8000u);
+    const bool zero = v[j] == 0.f;
+    float rest = fabsf(v[j]);
 #pragma unroll
-    for (int term = 0; term < (BF16 ? 3 : 2); ++term) {
-      const uint16_t t = BF16 ? f_to_bf16_bits(rest) : __half_as_ushort(__float2half_rn(rest));
-      put(term, r, t);
-      const float back = BF16 ? bf16_bits_to_f(t) : __half2float(__ushort_as_half(t));
-      rest = fabsf(back) < INFINITY ? rest - back : 0.f;
+    for (int term = 0; term < TERMS; ++term) {
+      const bool last = term == TERMS - 1;
+      uint16_t t;
+      float back;
+      if constexpr (BF16) {
+        t = last ? f_to_bf16_bits(rest) : (uint16_t)(__float_as_uint(rest * BELOW) >> 16);
+        back = bf16_bits_to_f(t);
+      } else {
+        // two steps are left at least where there are three, so that the last term rounds to nearest
+        const __half h = last ? __float2half_rn(rest) : __float2half_rz(fmaf(rest, BELOW, -2.f * STEP));
+        t = !zero && !(h > __float2half_rn(0.f)) && rest == rest ? 1 : __half_as_ushort(h);
+        back = __half2float(__ushort_as_half(t));
+      }
+      put(term, r, (uint16_t)(zero ? 0 : t | sign));
+      if (rest < INFINITY) rest -= back;  // an infinity or NaN: all terms
     }
   }
   return up;

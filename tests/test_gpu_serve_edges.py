@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import serve_ref as ref
-from test_gpu_serve import TYPES, Case, _num, _tq
+from test_gpu_serve import TYPES, Case, _lora_inputs, _num, _tq
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,29 @@ def test_attention_infinite_values(kind, strong):
             bound = ref.attention_bound(want, size, score, p + 1, 6.0, torch.float16, cache.k.dtype)
             ok = ~np.isinf(want)
             assert (np.abs(got[i, sl][ok] - want[ok]) <= bound[ok]).all(), (i, h)
+
+
+# ---- adapters ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [20, 300])
+def test_lora_infinite_b(kind, m):
+    """An infinity in B gives the infinity of its product with A x, also where A x is 2^-41 of the token's largest, and
+    stays in its output feature; times an A x of 0 it is NaN."""
+    tq = _tq()
+    x, a, b, s, ids, y = _lora_inputs(kind, m, 200, 512, 16, 2)
+    ids[:] = 1
+    a = (a.float() * 64).to(a.dtype)
+    x[:, 0], a[1, :, 0], a[1, 5], a[1, 6] = 2.0 ** -10, 0.0, 0.0, 0.0
+    a[1, 5, 0] = 2.0 ** -24
+    clean = tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y))
+    b = b.clone()
+    for n, r, v in ((7, 3, float("inf")), (9, 0, -float("inf")), (11, 5, float("inf")), (13, 6, float("inf"))):
+        b[1, n, r] = v
+    out = tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y))
+    h = _num(x) @ _num(a)[1].T
+    got = _num(out)
+    assert np.array_equal(got[:, 7], np.copysign(np.inf, h[:, 3])) and np.array_equal(got[:, 9], np.copysign(np.inf, -h[:, 0]))
+    assert (got[:, 11] == np.inf).all() and np.isnan(got[:, 13]).all()
+    keep = [n for n in range(200) if n not in (7, 9, 11, 13)]
+    assert torch.equal(out[:, keep], clean[:, keep])
