@@ -507,8 +507,8 @@ def tq_kv_append(cache: KvCache, qkv, q_heads: int, pos, freq=None, interleaved:
                  ws=None, stream=None):
     """Rotate and append new tokens.  qkv: float32 [m][(q_heads + 2 kv_heads) head_dim] (rows may be strided), pos:
     int32 [m] (-1 = a padded row), freq: float64 [rot/2] radians per position (None: no rotation), seq: int32 [m]
-    rows of the block table (None: token t is sequence t).  Returns the rotated queries [m][q_heads][head_dim]
-    (bfloat16 for a bfloat16 cache, else float16)."""
+    rows of the block table (None: token t is sequence t).  Two tokens of a call should not share a slot: their features
+    are mixed there.  Returns the rotated queries [m][q_heads][head_dim] (bfloat16 for a bfloat16 cache, else float16)."""
     import torch
     dev, m, D = cache.device, qkv.shape[0], cache.head_dim
     width = (q_heads + 2 * cache.kv_heads) * D

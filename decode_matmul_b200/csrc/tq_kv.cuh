@@ -68,7 +68,8 @@ __device__ __forceinline__ void flag_bad_index(int32_t* status) { atomicExch(sta
 // and has its next unit's loads under way.  The block's first threads form the
 // token's sines and cosines once for its heads.  Few tokens: the heads of each
 // are spread over blocks.  Many: blocks take whole tokens in turn, as many
-// blocks as run at once.
+// blocks as run at once.  Nothing orders the tokens: a slot that two of them
+// share gets each of its units from either.
 struct AppendParams {
   KvView c;
   const float* qkv;  // [m][qkv_stride]: q heads, k heads, v heads

@@ -425,8 +425,11 @@ typedef struct tq_kv_cache {
  * pos_d[t] < 0 marks a padded row: nothing is stored and its q_out row is 0.
  * A sequence, position or page outside the table or the cache stores nothing
  *   and leaves TQ_ERR_VALUE in the workspace's status word (q_out is written).
- *   Two tokens of a call with the same slot: one of them is kept, which one is
- *   not specified.  Every other byte of the cache is left as it was.
+ *   Two tokens of a call with the same slot: every feature of the slot's key
+ *   and value is one of theirs, which one's is not specified and may differ
+ *   from feature to feature (nothing orders the tokens of a call), so a caller
+ *   that needs one token whole gives only that one a position.  Every other
+ *   byte of the cache is left as it was.
  * freq_d: device fp64 [rot_dim/2], radians per position (fp64 so that far
  *   positions keep their angle); unused when rot_dim is 0.
  * rot_dim: a multiple of 16, 0 .. head_dim.  qkv_stride: elements, a multiple

@@ -24,6 +24,31 @@ def _rows(m, last):
     return pos, torch.zeros_like(pos)
 
 
+# ---- append --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m", [6, 640])
+def test_append_to_the_same_slot(kind, m):
+    """Tokens that share a slot: each feature of its key and value is one of theirs, every other slot is as it was, and
+    the queries are each token's own."""
+    tq = _tq()
+    hq, hk, d, page = 6, 3, 64, 16
+    cache = _cache(kind, torch.zeros((64, hk, d)), torch.zeros((64, hk, d)), page)
+    qkv = torch.from_numpy(np.random.default_rng(m).normal(size=(m, (hq + 2 * hk) * d)).astype(np.float32)).cuda()
+    pos, seq = _rows(m, 37)
+    pos[0] = 5  # and one that has its own
+    q = tq.tq_kv_append(cache, qkv, hq, pos, None, seq=seq)
+    x = qkv.view(m, hq + 2 * hk, d)
+    assert torch.equal(q, x[:, :hq].to(q.dtype))
+    for c, new in ((cache.k, x[:, hq:hq + hk]), (cache.v, x[:, hq + hk:])):
+        new = new.to(c.dtype).float()
+        c = c.float()
+        assert torch.equal(c[0, 5], new[0])
+        assert (c[37 // page, 37 % page] == new[1:]).any(dim=0).all()
+        c[0, 5] = c[37 // page, 37 % page] = 0.0
+        assert c.count_nonzero() == 0
+
+
 # ---- attention -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", list(TYPES))
