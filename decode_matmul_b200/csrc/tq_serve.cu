@@ -189,6 +189,18 @@ size_t lora_ws_bytes(const tq_lora_t* l, int32_t m) {
   return lora_mul_off(l, m) + (size_t)m * sizeof(float);
 }
 
+// What the query answers: enough for every call of up to m tokens.  (Fewer
+// tokens can need more, since they take more splits; within a number of tiles
+// the need grows with m.)
+size_t lora_ws_query(const tq_lora_t* l, int32_t m) {
+  size_t most = lora_ws_bytes(l, m);
+  for (int32_t t = m / tq::kLoraTile * tq::kLoraTile; t > tq::kLoraInBlock; t -= tq::kLoraTile) {
+    const size_t b = lora_ws_bytes(l, t);
+    if (b > most) most = b;
+  }
+  return most;
+}
+
 template <bool BF16, int PANELS>
 int lora_expand_launch(const tq::LoraParams& p, int sms, int64_t units, cudaStream_t stream) {
   auto kern = tq::lora_expand_kernel<BF16, PANELS>;
@@ -335,7 +347,7 @@ int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes) {
   int st = check_lora(lora);
   if (st != TQ_OK) return st;
   if (m < 0 || m > kMaxM) return TQ_ERR_SHAPE;
-  *bytes = lora_ws_bytes(lora, m);
+  *bytes = lora_ws_query(lora, m);
   return TQ_OK;
 }
 

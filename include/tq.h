@@ -502,7 +502,8 @@ typedef struct tq_lora {
  *   may be y_d (then with the same stride); any other overlap is not allowed.
  * Products are exact, sums are fp32, and A x keeps fp32 accuracy through the
  * second product.  0 <= m <= 4096 (m == 0: no launch).  Same workspace rules
- * as tq_gemv. */
+ * as tq_gemv; what tq_lora_workspace gives for m is enough for every smaller m
+ * too. */
 TQ_API int tq_lora_workspace(const tq_lora_t* lora, int32_t m, size_t* bytes);
 TQ_API int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* adapter_d, const float* y_d,
                    int64_t y_stride, float* out_d, int64_t out_stride, void* workspace_d, size_t ws_bytes,
