@@ -18,6 +18,8 @@ device, and a replay with new values in the same tensors is the next step.
 """
 from __future__ import annotations
 
+import math
+
 PHASE_OPS = (("q", "k", "v"), ("o",), ("gate", "up"), ("down",))
 
 
@@ -31,7 +33,9 @@ class AttentionStack:
 
     def __init__(self, layers, caches, freq=None, interleaved: bool = False, scale=None, window: int = 0,
                  adapters=None):
-        from . import OPS, layer_struct
+        import torch
+
+        from . import OPS, _need, layer_struct
         if not layers or len(caches) != len(layers) or (adapters is not None and len(adapters) != len(layers)):
             raise ValueError("one cache (and one dict of adapters) per layer is needed")
         c, w = caches[0], layers[0]
@@ -48,10 +52,20 @@ class AttentionStack:
                                      f"{want[op][0]} x {want[op][1]}")
             if (cache.kv_heads, cache.head_dim, cache.q_dtype, cache.device) != (c.kv_heads, c.head_dim, c.q_dtype, c.device):
                 raise ValueError("the caches of a stack have the same heads, type of queries and device")
+            if any(t.device != c.device for op in OPS for t in (L[op].codes, L[op].scales, L[op].codebook)):
+                raise ValueError(f"the weights of a stack are on its caches' device, {c.device}")
         for A, L in zip(adapters or (), layers):
             for op, lora in A.items():
                 if op not in PHASE_OPS[0] or (lora.n, lora.k) != (L[op].n, L[op].k):
                     raise ValueError(f"adapter on {op!r}: only q, k and v, of their projection's size")
+                if lora.a.dtype != torch.bfloat16 or lora.device != c.device:
+                    raise ValueError(f"adapter on {op!r}: bfloat16 on {c.device} is needed, got {lora.a.dtype} on {lora.device}")
+        if freq is not None:
+            _need(freq, "freq", torch.float64, (freq.numel(),), c.device)
+            if freq.numel() % 8 or 2 * freq.numel() > c.head_dim:
+                raise ValueError(f"freq: {freq.numel()} frequencies, a multiple of 8 and at most half of {c.head_dim} are needed")
+        if not 0 <= window < 2 ** 31 or (scale is not None and not math.isfinite(scale)):
+            raise ValueError(f"window {window} has to be 0 to 2^31 - 1 and scale {scale} finite")
         self.layers, self.caches, self.freq, self.interleaved, self.window = layers, caches, freq, interleaved, window
         self.scale = c.head_dim ** -0.5 if scale is None else scale
         self.adapters = adapters
@@ -96,7 +110,7 @@ class AttentionStack:
         tq_workspace_status(buffers(m)["ws"])."""
         import torch
 
-        from . import tq_attn, tq_kv_append, tq_layer_phase, tq_lora, tq_stack_phase_seed
+        from . import _need, tq_attn, tq_kv_append, tq_layer_phase, tq_lora, tq_stack_phase_seed
         if self.adapters is not None and adapter is None:
             raise ValueError("adapter: int32 [m] is needed, since the stack has adapters")
         m = h.shape[0]
@@ -106,6 +120,13 @@ class AttentionStack:
             out = torch.empty_like(h)
         elif out.dtype != h.dtype or out.shape != h.shape or not out.is_contiguous() or out.device != h.device:
             raise ValueError(f"out: like h, contiguous int16 {tuple(h.shape)} on {self.device}, is needed")
+        # all of them before the first launch: a step that is refused has written no cache
+        for name, t in (("pos", pos), ("seq", seq), ("adapter", adapter if self.adapters is not None else None)):
+            if t is not None:
+                _need(t, name, torch.int32, (m,), self.device)
+        rows = min(c.pages.shape[0] for c in self.caches)
+        if seq is None and m > rows:
+            raise ValueError(f"{m} tokens without seq, but the block tables have {rows} rows")
         if m == 0:
             return out
         b = self.buffers(m)

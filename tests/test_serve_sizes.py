@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import decode_matmul_b200 as tq
+from test_serve_args import _stack_parts
 
 
 def _lora(**kw):
@@ -36,3 +37,49 @@ def test_lora_workspace_covers_fewer_tokens(rank, k):
         # past the workspace check: no device here, or another kind
         assert _call_lora(lora, m, sizes[4096]) in (tq.TQ_ERR_CUDA, tq.TQ_ERR_ARCH) if not torch.cuda.is_available() else True
     assert _call_lora(lora, 3136, 65536) == tq.TQ_ERR_WORKSPACE
+
+
+def _adapter(n=128, dtype=torch.bfloat16, device="cpu"):
+    return tq.Lora(torch.zeros((1, 8, 512), dtype=dtype, device=device), torch.zeros((1, n, 8), dtype=dtype, device=device))
+
+
+def test_stack_refuses_what_a_step_could_not_take():
+    """Adapters of another type or device, weights on another device, frequencies, windows and scales that the calls of
+    a step would refuse: when the stack is made."""
+    from decode_matmul_b200.attention import AttentionStack
+    layers, caches = _stack_parts()
+    AttentionStack(layers, caches, torch.ones(32, dtype=torch.float64), adapters=[{"q": _adapter(256)}, {"v": _adapter()}])
+    for lora in (_adapter(dtype=torch.float16), _adapter(device="meta")):
+        with pytest.raises(ValueError):
+            AttentionStack(layers, caches, adapters=[{}, {"k": lora}])
+    far = torch.zeros(0, device="meta")
+    for part in ((far, torch.zeros(0), torch.zeros(0)), (torch.zeros(0), far, torch.zeros(0)), (torch.zeros(0), torch.zeros(0), far)):
+        other = [layers[0], {**layers[1], "up": tq.DeviceWeight(*part, 1024, 512)}]
+        with pytest.raises(ValueError):
+            AttentionStack(other, caches)
+    for kw in (dict(freq=torch.ones(32)), dict(freq=torch.ones(12, dtype=torch.float64)), dict(freq=torch.ones(40, dtype=torch.float64)),
+               dict(freq=torch.ones(8, dtype=torch.float64, device="meta")), dict(window=-1), dict(window=2 ** 31),
+               dict(scale=float("inf")), dict(scale=float("nan"))):
+        with pytest.raises(ValueError):
+            AttentionStack(layers, caches, **kw)
+
+
+def test_stack_refuses_a_step_before_its_first_launch(monkeypatch):
+    """Positions, sequences and adapter indices of the wrong type, size or device, and more tokens than block-table rows
+    in any layer: before the buffers are made, so no cache is written."""
+    from decode_matmul_b200.attention import AttentionStack
+    layers, caches = _stack_parts()
+    caches[1] = tq.KvCache(caches[1].k, caches[1].v, torch.zeros((1, 3), dtype=torch.int32))
+    stack = AttentionStack(layers, caches, adapters=[{}, {"k": _adapter()}])
+
+    def reached(m):
+        raise AssertionError("the step began")
+
+    monkeypatch.setattr(stack, "buffers", reached)
+    h, i = torch.zeros((2, 512), dtype=torch.int16), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(AssertionError):
+        stack.forward(h, i, 0, seq=i, adapter=i)
+    for pos, seq, ids in ((i.long(), i, i), (i[:1], i, i), (i, i.long(), i), (i, i[:1], i), (i, i, i.long()), (i, i, i[:1]),
+                          (i.to("meta"), i, i), (i, i.to("meta"), i), (i, i, i.to("meta")), (i, None, i)):
+        with pytest.raises(ValueError):
+            stack.forward(h, pos, 0, seq=seq, adapter=ids)
