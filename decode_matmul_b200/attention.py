@@ -71,36 +71,45 @@ class AttentionStack:
         self.adapters = adapters
         self.device = c.device
         self.structs = [layer_struct(L) for L in layers]
-        self._buf = {}
+        self._buf = {}    # sets of buffers by the most tokens they take
+        self._views = {}  # their first m rows, by m
 
     def buffers(self, m: int) -> dict:
         """The workspace and activation buffers of steps of m tokens (kept; the last layer's values stay in them
-        after a step: y, q, attn and the phases' handoffs).  All steps of m tokens share them, so those follow one
-        another on one stream.  A captured step's must exist before the capture, from an earlier step or this call:
-        what a capture clears is clear only when it is replayed."""
+        after a step: y, q, attn and the phases' handoffs).  Steps of up to 16, of 17 to 32, 33 to 64, ... tokens share
+        one set, of which a step uses the first m rows (so that all sets together are at most twice the largest,
+        however many numbers of tokens there are), so those follow one another on one stream.  A captured step's must
+        exist before the capture, from an earlier step or this call: what a capture clears is clear only when it is
+        replayed."""
         import torch
 
         from . import tq_attn_workspace, tq_layer_phase_workspace, tq_lora_workspace, workspace
-        if m in self._buf:
-            return self._buf[m]
-        with torch.cuda.device(self.device):  # on whose current stream the workspace is cleared
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError(f"buffers({m}) has to be called before a step of {m} tokens is captured")
-            n = max(tq_layer_phase_workspace(s, p, m) for s in self.structs for p in range(4))
-            n = max([n] + [tq_attn_workspace(c, m, self.q_heads) for c in self.caches]
-                    + [tq_lora_workspace(a, m) for A in self.adapters or () for a in A.values()])
-            w, c, dev = self.layers[0], self.caches[0], self.device
+        if m in self._views:
+            return self._views[m]
+        most = max(16, 1 << (m - 1).bit_length())
+        if most not in self._buf:
+            n = max(tq_attn_workspace(c, m, self.q_heads) for c in self.caches)  # refuses too many tokens
+            with torch.cuda.device(self.device):  # on whose current stream the workspace is cleared
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError(f"buffers({m}) has to be called before a step of {m} tokens is captured")
+                # (the phases of all layers have the same sizes; fewer tokens can need more)
+                n = max([n] + [tq_layer_phase_workspace(self.structs[0], p, i) for p in range(4)
+                               for i in range(most // 2 + 1 if most > 16 else 1, most + 1)]
+                        + [tq_lora_workspace(a, most) for A in self.adapters or () for a in A.values()])
+                w, c, dev = self.layers[0], self.caches[0], self.device
 
-            def bits(width):
-                return torch.empty((m, width), dtype=torch.int16, device=dev)
+                def bits(width):
+                    return torch.empty((most, width), dtype=torch.int16, device=dev)
 
-            heads = (m, self.q_heads, c.head_dim)
-            self._buf[m] = dict(
-                ws=workspace(n, dev), y=torch.empty((m, sum(w[o].n for o in PHASE_OPS[0])), device=dev),
-                q=torch.empty(heads, dtype=c.q_dtype, device=dev),
-                attn=torch.empty(heads, dtype=torch.bfloat16, device=dev),
-                hand=[bits(w["q"].n), bits(w["o"].n), bits(w["gate"].n), bits(w["down"].n)])
-        return self._buf[m]
+                heads = (most, self.q_heads, c.head_dim)
+                self._buf[most] = dict(
+                    ws=workspace(n, dev), y=torch.empty((most, sum(w[o].n for o in PHASE_OPS[0])), device=dev),
+                    q=torch.empty(heads, dtype=c.q_dtype, device=dev),
+                    attn=torch.empty(heads, dtype=torch.bfloat16, device=dev),
+                    hand=[bits(w["q"].n), bits(w["o"].n), bits(w["gate"].n), bits(w["down"].n)])
+        b = self._buf[most]
+        self._views[m] = dict(ws=b["ws"], hand=[t[:m] for t in b["hand"]], **{k: b[k][:m] for k in ("y", "q", "attn")})
+        return self._views[m]
 
     def forward(self, h, pos, seed: int, seq=None, adapter=None, out=None):
         """One step of m new tokens.  h: int16 (bf16 bits) [m][hidden]; pos: int32 [m], the tokens' positions (-1 = a

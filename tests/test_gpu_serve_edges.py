@@ -166,3 +166,35 @@ def test_lora_infinite_b(kind, m):
     assert (got[:, 11] == np.inf).all() and np.isnan(got[:, 13]).all()
     keep = [n for n in range(200) if n not in (7, 9, 11, 13)]
     assert torch.equal(out[:, keep], clean[:, keep])
+
+
+# ---- the stack -----------------------------------------------------------------------
+
+def test_stack_steps_of_different_sizes_share_buffers():
+    """Steps of 5 and 3 tokens, eager and replayed from a graph, in turn on one set of buffers, give the bits that
+    stacks of their own give."""
+    import tqsynth
+    from decode_matmul_b200.attention import AttentionStack
+    tq = _tq()
+    shape = tqsynth.StackShape("share-test", 1, 512, 1024, 256, 1536)
+    cb = tqsynth.codebook(3)
+    cbd = torch.from_numpy(cb.view(np.int16)).cuda()
+    host = {op: tqsynth.Weight(3, 0, i, n, k, cb) for i, (op, n, k) in enumerate(shape.ops())}
+    layers = [{op: tq.DeviceWeight.from_host(w.codes, w.scales, cbd, w.n, w.k) for op, w in host.items()}]
+    cases = [Case(9, "bf16", 128, 8, 2, 16, [40, 3, 17, 30, 9], shuffle_seq=False) for _ in range(3)]
+    h = torch.from_numpy(tqsynth.activations(1, 5, 512).view(np.int16)).cuda()
+    pos = cases[0].pos_d
+    alone = [AttentionStack(layers, [c.cache]).forward(h[:m], pos[:m], 5) for c, m in zip(cases, (5, 3))]
+    stack = AttentionStack(layers, [cases[2].cache])
+    out5, out3 = torch.empty_like(h), torch.empty_like(h[:3])
+    stack.forward(h, pos, 5, out=out5)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        stack.forward(h[:3], pos[:3], 5, out=out3)
+    for _ in range(2):
+        out5.zero_()
+        out3.zero_()
+        g.replay()
+        stack.forward(h, pos, 5, out=out5)
+        assert torch.equal(out5, alone[0]) and torch.equal(out3, alone[1])
+    assert tq.tq_workspace_status(stack.buffers(3)["ws"]) == tq.TQ_OK

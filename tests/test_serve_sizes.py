@@ -1,5 +1,6 @@
 """Argument checks and host-side rules of the cache, attention and adapter
 calls that need no GPU, where sizes or arguments interact."""
+import contextlib
 import ctypes
 
 import pytest
@@ -83,3 +84,37 @@ def test_stack_refuses_a_step_before_its_first_launch(monkeypatch):
                           (i.to("meta"), i, i), (i, i.to("meta"), i), (i, i, i.to("meta")), (i, None, i)):
         with pytest.raises(ValueError):
             stack.forward(h, pos, 0, seq=seq, adapter=ids)
+
+
+def test_stack_buffers_stay_bounded(monkeypatch):
+    """Every number of tokens in turn holds no more than twice the largest set, each with rows of its own size and a
+    workspace that every call of its step takes."""
+    from decode_matmul_b200.attention import AttentionStack
+    shape = dict(q=(512, 512), k=(128, 512), v=(128, 512), o=(512, 512), gate=(1024, 512), up=(1024, 512), down=(512, 1024))
+    some = torch.zeros(16)  # an address: nothing reads it
+    layers = [{op: tq.DeviceWeight(some, some, some, *s) for op, s in shape.items()} for _ in range(2)]
+    caches = _stack_parts()[1]
+    lora = _adapter()
+    stack = AttentionStack(layers, caches, adapters=[{"k": lora}, {}])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(tq, "workspace", lambda n, dev: torch.empty(n, dtype=torch.uint8, device=dev))
+    held = {}
+    for m in [1, 2, 15, 16, 17, 33, 64, 65] + list(range(100, 4097, 111)) + [4096, 3, 2000]:
+        b = stack.buffers(m)
+        assert stack.buffers(m) is b
+        assert b["y"].shape == (m, 768) and b["q"].shape == b["attn"].shape == (m, 8, 64)
+        assert [tuple(t.shape) for t in b["hand"]] == [(m, 512), (m, 512), (m, 1024), (m, 512)]
+        need = [tq.tq_layer_phase_workspace(s, p, m) for s in stack.structs for p in range(4)]
+        need += [tq.tq_attn_workspace(c, m, 8) for c in caches] + [tq.tq_lora_workspace(lora, m), 65536]
+        assert b["ws"].numel() >= max(need)
+        for t in [b["ws"], b["y"], b["q"], b["attn"]] + b["hand"]:
+            assert t.is_contiguous() and t.data_ptr() % 16 == 0
+            held[t.untyped_storage().data_ptr()] = t.untyped_storage().nbytes()
+    largest = stack.buffers(4096)
+    largest = sum(t.untyped_storage().nbytes() for t in [largest["ws"], largest["y"], largest["q"], largest["attn"]] + largest["hand"])
+    # the sets of 16, 32, ... 2048 tokens: half, a quarter, ... of the activations; workspaces also hold fixed parts
+    fixed = 9 * tq.tq_attn_workspace(caches[0], 1, 8) + 9 * (4 << 20)
+    assert sum(held.values()) <= 2 * largest + fixed
+    with pytest.raises(tq.TqError):
+        stack.buffers(4097)
