@@ -357,6 +357,7 @@ int tq_lora(const tq_lora_t* lora, const void* x_d, int32_t m, const int32_t* ad
   if (st != TQ_OK) return st;
   if (m < 0 || m > kMaxM || y_stride < lora->n || out_stride < lora->n) return TQ_ERR_SHAPE;
   if (y_stride > (1 << 20) || out_stride > (1 << 20)) return TQ_ERR_SHAPE;  // m rows stay inside 32-bit offsets
+  if (m > 1 && out_d == y_d && out_stride != y_stride) return TQ_ERR_SHAPE;  // rows would be overwritten before they are read
   if (m == 0) return TQ_OK;
   if (!x_d || !adapter_d || !y_d || !out_d) return TQ_ERR_NULL;
   if (!aligned16(x_d) || !aligned_to(adapter_d, 4) || !aligned_to(y_d, 4) || !aligned_to(out_d, 4)) return TQ_ERR_ALIGN;

@@ -499,7 +499,8 @@ typedef struct tq_lora {
  * y_d, out_d: device fp32, row t at t * y_stride / t * out_stride elements
  *   (n .. 2^20), 4-byte aligned (16-byte alignment and strides of a multiple of 4
  *   are faster), so q, k or v columns of a phase's y can be addressed.  out_d
- *   may be y_d (then with the same stride); any other overlap is not allowed.
+ *   may be y_d (then with the same stride, TQ_ERR_SHAPE otherwise); any other
+ *   overlap is not allowed.
  * Products are exact, sums are fp32, and A x keeps fp32 accuracy through the
  * second product.  0 <= m <= 4096 (m == 0: no launch).  Same workspace rules
  * as tq_gemv; what tq_lora_workspace gives for m is enough for every smaller m

@@ -40,6 +40,15 @@ def test_lora_workspace_covers_fewer_tokens(rank, k):
     assert _call_lora(lora, 3136, 65536) == tq.TQ_ERR_WORKSPACE
 
 
+def test_lora_in_place_needs_equal_strides():
+    """Output rows over other rows of y: refused (one row has no stride)."""
+    lora = _lora()
+    assert _call_lora(lora, 3, 1 << 40, y=16, out=16, ys=1000, os=1004) == tq.TQ_ERR_SHAPE
+    if not torch.cuda.is_available():  # past the checks: no device here, or another kind
+        assert _call_lora(lora, 1, 1 << 40, y=16, out=16, ys=1000, os=1004) in (tq.TQ_ERR_CUDA, tq.TQ_ERR_ARCH)
+        assert _call_lora(lora, 3, 1 << 40, y=16, out=1 << 30, ys=1000, os=1004) in (tq.TQ_ERR_CUDA, tq.TQ_ERR_ARCH)
+
+
 def _adapter(n=128, dtype=torch.bfloat16, device="cpu"):
     return tq.Lora(torch.zeros((1, 8, 512), dtype=dtype, device=device), torch.zeros((1, n, 8), dtype=dtype, device=device))
 
