@@ -562,6 +562,8 @@ def tq_attn(cache: KvCache, q, pos, scale: float, seq=None, window: int = 0, out
         _need(seq, "seq", torch.int32, (m,), dev)
     elif m > cache.pages.shape[0]:
         raise ValueError(f"{m} rows without seq, but the block table has {cache.pages.shape[0]} rows")
+    if not -2 ** 31 <= window < 2 ** 31:  # would wrap into another window on its way to C
+        raise ValueError(f"window {window}: 0 to 2^31 - 1 is needed")
     if out is not None:
         out_dtype = TQ_F16 if out.dtype is torch.float16 else TQ_BF16
         _need(out, "out", torch.float16 if out_dtype == TQ_F16 else torch.bfloat16, q.shape, dev)

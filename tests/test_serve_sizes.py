@@ -49,6 +49,16 @@ def test_lora_in_place_needs_equal_strides():
         assert _call_lora(lora, 3, 1 << 40, y=16, out=1 << 30, ys=1000, os=1004) in (tq.TQ_ERR_CUDA, tq.TQ_ERR_ARCH)
 
 
+def test_attn_refuses_windows_beyond_32_bits():
+    """2^32 + 5 would arrive as a window of 5."""
+    k = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    cache = tq.KvCache(k, k.clone(), torch.zeros((2, 3), dtype=torch.int32))
+    q, pos = torch.zeros((2, 4, 64), dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for window in (2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5):
+        with pytest.raises(ValueError, match="window"):
+            tq.tq_attn(cache, q, pos, 0.1, window=window)
+
+
 def _adapter(n=128, dtype=torch.bfloat16, device="cpu"):
     return tq.Lora(torch.zeros((1, 8, 512), dtype=dtype, device=device), torch.zeros((1, n, 8), dtype=dtype, device=device))
 
