@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   int32_t b0, share, rest, blocks;  // block c takes share units, one more when c < rest
   int32_t wshare, wrest;            // and so its teams
   int team, items, teams, my_team, member;  // items: of a team
-  // false: this block has nothing to do.  A call of 2^31 units (30 TB of
-  // keys and values and more) is refused.
+  // false: this block has nothing to do.  A call of 2^31 units (16 TB of
+  // keys and values and more) is refused: zeros.
   auto split = [&](int64_t rows_total) {
     items = p.c.kv_heads * p.head_groups;
     // teams leave more parts to join: not worth it for blocks with little work
@@ -405,6 +405,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
     member = warp - my_team * team;
     if (rows_total > 0x7fffffffll / items) {
       if (tid == 0 && blockIdx.x == 0) flag_bad_index(p.status);
+      uint4* out = static_cast<uint4*>(p.out);
+      const int64_t n = (int64_t)p.m * p.q_heads * (D / 8);
+      for (int64_t i = (int64_t)blockIdx.x * C::THREADS + tid; i < n; i += (int64_t)gridDim.x * C::THREADS)
+        out[i] = make_uint4(0, 0, 0, 0);
       return false;
     }
     const int32_t total = (int32_t)rows_total * items, c = blockIdx.x;

@@ -459,6 +459,9 @@ TQ_API int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t 
  * A sequence or position outside the table makes its row see no key, a page
  *   index outside the cache hides that page's keys; both leave TQ_ERR_VALUE in
  *   the status word.
+ * A call whose rows see 2^31 tiles or more, of 16 keys of a key head each
+ *   and five at least for a row and head (2^35 keys, 16 TB), can be too large:
+ *   it then gives zeros and leaves TQ_ERR_VALUE in the status word.
  * Rows may share a sequence (several new tokens of one request, each with its
  *   own position); each reads the cache for itself.
  * The keys of a long row are split over the GPU and joined in the same launch,

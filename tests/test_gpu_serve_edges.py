@@ -142,6 +142,25 @@ def test_attention_infinite_values(kind, strong):
             assert (np.abs(got[i, sl][ok] - want[ok]) <= bound[ok]).all(), (i, h)
 
 
+def test_attention_of_too_many_tiles():
+    """4096 rows of 2^20 keys on 32 key heads (a table that names one page again and again): zeros and the status."""
+    tq = _tq()
+    m, hk, n = 4096, 32, 1 << 20
+    k = torch.zeros((1, 64, hk, 64), dtype=torch.float16, device="cuda")
+    cache = tq.KvCache(k, torch.ones_like(k), torch.zeros((1, n // 64), dtype=torch.int32, device="cuda"))
+    pos, seq = _rows(m, n - 1)
+    q = torch.zeros((m, hk, 64), dtype=torch.float16, device="cuda")
+    out = torch.full((m, hk, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = tq.workspace(tq.tq_attn_workspace(cache, m, hk))
+    tq.tq_attn(cache, q, pos, 1.0, seq, out=out, ws=ws)
+    assert tq.tq_workspace_status(ws) == tq.TQ_ERR_VALUE
+    assert out.count_nonzero() == 0 and (ws[:65532] == 0).all()
+    # with a window they are few: as ever
+    ws = tq.workspace(tq.tq_attn_workspace(cache, m, hk))
+    tq.tq_attn(cache, q, pos, 1.0, seq, 100, out=out, ws=ws)
+    assert tq.tq_workspace_status(ws) == tq.TQ_OK and (out == 1).all()
+
+
 # ---- adapters ------------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
