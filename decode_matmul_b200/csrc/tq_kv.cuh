@@ -236,7 +236,8 @@ __global__ void __launch_bounds__(AP_THREADS, append_blocks(T)) append_kernel(Ap
       } else {
         const float* sp = is_v ? p.c.vs : p.c.ks;
         const float scale = sp ? sp[kvh] : 1.f, inv = 1.f / scale;
-        const bool odd_scale = !(fabsf(inv) < INFINITY);  // 0, NaN or below 2^-128: exact forms only
+        // exact forms only: scales of 0 or NaN, and those whose values or reciprocals may be subnormal (fewer bits)
+        const bool odd_scale = !(fabsf(inv) >= 0x1p-100f && fabsf(inv) <= 0x1p100f);
         uint8_t* dst = static_cast<uint8_t*>(base) + o;
 #pragma unroll
         for (int run = 0; run < 2; ++run) {

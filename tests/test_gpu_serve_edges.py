@@ -49,6 +49,30 @@ def test_append_to_the_same_slot(kind, m):
         assert c.count_nonzero() == 0
 
 
+def test_append_e4m3_scales_at_the_ends_of_binary32():
+    """Values at and next to every tie between e4m3 values, for scales whose values or reciprocals are subnormal: the
+    byte nearest to the exact quotient."""
+    tq = _tq()
+    scales = np.array([2.0 ** -125 * 1.0613, 2.0 ** -126.5 * 1.077, 2.0 ** -127.5 * 1.07, 2.0 ** -101, 2.0 ** 126.9, 2.0 ** 127.8],
+                      dtype=np.float32)
+    ties = np.array([(8 + i + 0.5) * 2.0 ** j for i in range(8) for j in range(-12, 6)])
+    d, rows = 64, 12
+    x = np.zeros((rows, 3, len(scales), d), dtype=np.float32)
+    for h, s in enumerate(scales):
+        mid = (ties * float(s))[ties * float(s) < 3e38].astype(np.float32)
+        near = [mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(np.inf))]
+        near = np.resize(np.stack(near + [-near[1]], 1).ravel(), rows * d).reshape(rows, d)
+        x[:, 1, h] = x[:, 2, h] = near
+    cache = _cache("e4m3", torch.zeros((64, len(scales), d)), torch.zeros((64, len(scales), d)))
+    s_d = torch.from_numpy(scales).cuda()
+    cache = tq.KvCache(cache.k, cache.v, cache.pages, s_d, s_d)
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    tq.tq_kv_append(cache, torch.from_numpy(x.reshape(rows, -1)).cuda(), len(scales), pos, None, seq=torch.zeros_like(pos))
+    want = ref.round_e4m3(x[:, 1].astype(np.float64) / scales.astype(np.float64)[:, None])
+    for c in (cache.k, cache.v):
+        assert np.array_equal(_num(c[0, :rows]), want)
+
+
 # ---- attention -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", list(TYPES))
