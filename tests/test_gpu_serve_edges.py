@@ -73,6 +73,58 @@ def test_append_e4m3_scales_at_the_ends_of_binary32():
         assert np.array_equal(_num(c[0, :rows]), want)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("hq,hk,d,rot,inter", [(3, 3, 64, 64, False), (20, 4, 128, 128, True), (8, 1, 256, 64, False)])
+def test_append_of_many_tokens(kind, hq, hk, d, rot, inter):
+    """A prompt in which blocks take whole tokens, from half as many tokens as there are blocks at once to several per
+    block, with padded rows and indices out of range among the others."""
+    tq = _tq()
+    at_once = torch.cuda.get_device_properties(0).multi_processor_count * (5 if kind == "e4m3" else 7)
+    n, page = 4224, 32
+    rng = np.random.default_rng(hq)
+    table = rng.permutation(n // page).astype(np.int32)
+    freq = np.exp(-rng.uniform(0, 14, rot // 2))
+    scale = (rng.uniform(0.5, 1.5, hk) / 100).astype(np.float32)
+    i = np.arange(rot // 2)
+    lo, hi = (2 * i, 2 * i + 1) if inter else (i, i + rot // 2)
+    for m in (at_once // 2 - 1, at_once // 2, at_once // 2 + 1, at_once, at_once + 1, 2 * at_once + 7, 4096):
+        pos = rng.permutation(n)[:m].astype(np.int32)
+        seq = np.zeros(m, dtype=np.int32)
+        bad = rng.permutation(m)[:40]
+        pos[bad[:16]] = -1
+        seq[bad[16:24]], seq[bad[24:32]], pos[bad[32:]] = -1, 1, n + bad[32:]
+        live = np.ones(m, dtype=bool)
+        live[bad] = False
+        x = rng.normal(size=(m, hq + 2 * hk, d)).astype(np.float32)
+        k, v = (torch.zeros((n // page, page, hk, d)).to(TYPES[kind]).cuda() for _ in range(2))
+        s_d = torch.from_numpy(scale).cuda() if kind == "e4m3" else None
+        cache = tq.KvCache(k, v, torch.from_numpy(table).cuda().view(1, -1), s_d, s_d)
+        ws = tq.workspace(tq.tq_kv_append_workspace())
+        q = tq.tq_kv_append(cache, torch.from_numpy(x.reshape(m, -1)).cuda(), hq, torch.from_numpy(pos).cuda(),
+                            torch.from_numpy(freq).cuda(), inter, torch.from_numpy(seq).cuda(), ws=ws)
+        assert tq.tq_workspace_status(ws) == tq.TQ_ERR_VALUE
+        turned = x.astype(np.float64)
+        angle = pos[:, None, None] * freq
+        c, s, e = np.cos(angle), np.sin(angle), turned[:, :hq + hk]
+        e[..., lo], e[..., hi] = e[..., lo] * c - e[..., hi] * s, e[..., lo] * s + e[..., hi] * c
+        size = ref.rotation_size(x[:, :hq + hk].astype(np.float64), rot // 2, inter) * 2.0 ** -21  # as in _check_append
+        turned[pos < 0, :hq], size[pos < 0, :hq] = 0.0, 0.0
+        half = torch.finfo(q.dtype).eps / 2
+        tiny = 2.0 ** -25 if q.dtype == torch.float16 else 0.0
+        assert (np.abs(_num(q) - turned[:, :hq]) <= np.abs(turned[:, :hq]) * half + size[:, :hq] * 1.01 + tiny).all(), m
+        for got, new, far in ((k, turned[:, hq:hq + hk], size[:, hq:]), (v, turned[:, hq + hk:], 0.0)):
+            got = _num(got).reshape(n, hk, d)
+            at = table[pos[live] // page] * page + pos[live] % page
+            if kind == "e4m3":
+                assert np.array_equal(got[at], ref.round_e4m3(new[live] / scale.astype(np.float64)[:, None])), m
+            else:
+                far = far[live] * 1.01 if isinstance(far, np.ndarray) else far
+                assert (np.abs(got[at] - new[live]) <= np.abs(new[live]) * half + far + tiny).all(), m
+            rest = np.ones(n, dtype=bool)
+            rest[at] = False
+            assert (got[rest] == 0).all(), m
+
+
 # ---- attention -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("kind", list(TYPES))
@@ -209,6 +261,61 @@ def test_lora_infinite_b(kind, m):
     assert (got[:, 11] == np.inf).all() and np.isnan(got[:, 13]).all()
     keep = [n for n in range(200) if n not in (7, 9, 11, 13)]
     assert torch.equal(out[:, keep], clean[:, keep])
+
+
+@pytest.mark.parametrize("kind,m,n,k,rank", [
+    ("f16", 8, 512, 17408, 128), ("bf16", 8, 512, 17408, 128), ("f16", 300, 512, 17408, 128), ("bf16", 300, 300, 14336, 72),
+    ("f16", 1, 1024, 2560, 16), ("bf16", 64, 700, 2560, 64), ("bf16", 1000, 256, 1024, 64), ("f16", 1000, 256, 1024, 24),
+])
+def test_lora_keeps_32_bits(kind, m, n, k, rank):
+    """The adapters' part alone (y = 0), by norms: 1.2e-6.  A tensor core's sum loses up to 2^-23 of itself per MMA, half
+    of that on average and two thirds of its final size over a chain, so a chain of 24 loses 24 x 2^-23 / 3 = 9.5e-7 of
+    it; the chains of A x have either sign and add up like their parts do.  Both products together: less than sqrt(2)
+    times that, and chains of 16 in one of the two in most cases.  (An A x of 16 bits would leave 7.6e-6, and chains of
+    136 MMAs over 17408 features gave 2.5e-6.)"""
+    tq = _tq()
+    x, a, b, s, ids, y = _lora_inputs(kind, m, n, k, rank, 3)
+    y.zero_()
+    out = tq.tq_lora(tq.Lora(a, b, s), x, ids.cuda(), y, out=torch.empty_like(y))
+    want = torch.zeros((m, n), dtype=torch.float64, device="cuda")
+    for ad in range(3):
+        t = (ids == ad).nonzero()[:, 0].cuda()
+        want[t] = s[ad].double() * ((x[t].double() @ a[ad].double().T) @ b[ad].double().T)
+    assert float((out.double() - want).norm() / want.norm().clamp(min=1e-30)) <= 1.2e-6
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 20, 300])
+def test_lora_terms_of_one_element(kind, m):
+    """A x made of two or three products whose bits do not overlap, and B the identity: the output is A x, to 2^-19
+    (2^-22 for two fp16 terms, and four sums that lose 2^-22).  A term less leaves 2^-18 (bf16) or 2^-12 (fp16)."""
+    tq = _tq()
+    rank, k, g = 128, 1024, torch.Generator().manual_seed(m)
+    t = TYPES[kind]
+    parts, bits = (3, 8) if kind == "bf16" else (2, 11)
+    a = torch.zeros((1, rank, k))
+    for i in range(parts):
+        a[0, :, 37 * i + 5] = (torch.rand(rank, generator=g) + 1) * 2.0 ** (-bits * i)
+    x = torch.zeros((m, k))
+    x[:, [37 * i + 5 for i in range(parts)]] = 1.0
+    a, x, b = a.to(t).cuda(), x.to(t).cuda(), torch.eye(rank).to(t).cuda()[None].contiguous()
+    y = torch.zeros((m, rank), device="cuda")
+    out = tq.tq_lora(tq.Lora(a, b), x, torch.zeros(m, dtype=torch.int32, device="cuda"), y)
+    want = x.double() @ a[0].double().T
+    assert float(((out.double() - want).abs() / want).max()) <= 2.0 ** -19
+
+
+def test_lora_tokens_by_themselves():
+    """A token's output has the same bits wherever it stands among tokens of its adapter that fill the same tiles."""
+    tq = _tq()
+    for m in (24, 320):
+        x, a, b, s, ids, y = _lora_inputs("bf16", m, 200, 1024, 16, 2)
+        ids[:] = 1
+        lora = tq.Lora(a, b, s)
+        out = tq.tq_lora(lora, x, ids.cuda(), y, out=torch.empty_like(y))
+        order = torch.randperm(m, generator=torch.Generator().manual_seed(m))
+        back = tq.tq_lora(lora, x[order].contiguous(), ids.cuda(), y[order].contiguous())
+        assert torch.equal(back, out[order])
 
 
 # ---- the stack -----------------------------------------------------------------------
