@@ -68,7 +68,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
 
 constexpr int LORA_THREADS = 256;
 constexpr int LORA_CLUSTER = 8;
-constexpr int kLoraInBlock = 256;  // up to this many tokens each block groups them for itself
+// Up to this many tokens each block groups them for itself (a thread per token)
+// and the call is one launch.  One against three launches, n = 4096, k = 14336,
+// rank 16: 64 tokens of 40 adapters 12.8 against 28.2 us, 256 of 40 17.5 against
+// 29.7, 256 of one 13.7 against 17.0.  Where A and B read once per 8 tokens
+// outweigh that, the rule costs: n = 19456, k = 2560, rank 64, 64 tokens of one
+// 22.6 against 20.0, 256 of 40 55.7 against 54.2, 256 of one 43.3 against 27.9.
+constexpr int kLoraInBlock = 256;
 constexpr int kLoraSmall = 8;      // tokens of a tile up to kLoraInBlock, and beyond
 constexpr int kLoraTile = 32;
 constexpr int kLoraMaxM = 4096;
@@ -311,116 +317,94 @@ __device__ __forceinline__ void lora_shrink(const LoraParams& p, int32_t ad, int
 }
 
 // Step 3 for up to 8 tokens: this warp's groups of 32 features, e0, e0 + step,
-// ... below e1, GN at a time with all their loads in flight (B 32 ranks at a
-// time, the next while these are multiplied).  One at a time and two pieces of
-// A in step 1 leave registers for four blocks per SM: against two blocks with
-// twice as much in flight each, 250 tokens of 48 adapters 41 -> 30 us, 16 of 8
-// 11.2 -> 10.7, 64 of 24 16.8 -> 17.4.
+// ... below e1, one at a time (B 32 ranks at a time, the next while these are
+// multiplied).  One group and two pieces of A in step 1 leave registers for
+// four blocks per SM: against two blocks with twice as much in flight each, 250
+// tokens of 48 adapters 41 -> 30 us, 16 of 8 11.2 -> 10.7, 64 of 24 16.8 -> 17.4.
 template <bool BF16, bool VEC>
 __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, int e0, int e1, int step, const int32_t* tok,
                                              int cnt, const uint16_t* planes, int pstride, const float* mul) {
-  constexpr int GN = 1, AHEAD = 2;
+  constexpr int AHEAD = 2;
   constexpr int TERMS = BF16 ? 3 : 2;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   // MMA rows g, g + 8 of the two row tiles are features 4g .. 4g + 3
   const uint16_t* bp = static_cast<const uint16_t*>(p.b) + (int64_t)ad * p.n * p.rank + q * 4;
-  for (int e = e0; e < e1; e += GN * step) {
-    uint2 b[GN][AHEAD][4];
+  for (int e = e0; e < e1; e += step) {
+    const int f = e * 32 + 4 * g;
+    uint2 b[AHEAD][4];
     auto load_b = [&](int r0) {
 #pragma unroll
-      for (int j = 0; j < GN; ++j) {
-        const int f = (e + j * step) * 32 + 4 * g;
-        const bool on = e + j * step < e1;
+      for (int u = 0; u < AHEAD; ++u) {
+        const int r = r0 + u * 16;
+        const bool in = r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u) {
-          const int r = r0 + u * 16;
-          const bool in = on && r + q * 4 < p.rank;  // false too in the last 8 of an odd number of eights
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            b[j][u][i] = in && f + i < p.n ? *reinterpret_cast<const uint2*>(bp + (int64_t)(f + i) * p.rank + r)
-                                           : make_uint2(0, 0);
-        }
+        for (int i = 0; i < 4; ++i)
+          b[u][i] = in && f + i < p.n ? *reinterpret_cast<const uint2*>(bp + (int64_t)(f + i) * p.rank + r) : make_uint2(0, 0);
       }
     };
     load_b(0);
-    float4 yv[GN][2];
+    float4 yv[2];
 #pragma unroll
-    for (int j = 0; j < GN; ++j) {
-      const int f = (e + j * step) * 32 + 4 * g;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = q * 2 + i;
-        float4& v = yv[j][i];
-        v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (e + j * step < e1 && c < cnt && f < p.n) {
-          const float* src = p.y + tok[c] * p.y_stride + f;
-          if (VEC && f + 4 <= p.n) {
-            v = *reinterpret_cast<const float4*>(src);
-          } else {
-            v.x = src[0];
-            if (f + 1 < p.n) v.y = src[1];
-            if (f + 2 < p.n) v.z = src[2];
-            if (f + 3 < p.n) v.w = src[3];
-          }
+    for (int i = 0; i < 2; ++i) {
+      const int c = q * 2 + i;
+      float4& v = yv[i];
+      v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c < cnt && f < p.n) {
+        const float* src = p.y + tok[c] * p.y_stride + f;
+        if (VEC && f + 4 <= p.n) {
+          v = *reinterpret_cast<const float4*>(src);
+        } else {
+          v.x = src[0];
+          if (f + 1 < p.n) v.y = src[1];
+          if (f + 2 < p.n) v.z = src[2];
+          if (f + 3 < p.n) v.w = src[3];
         }
       }
     }
-    float acc[GN][2][4];
+    float acc[2][4];
 #pragma unroll
-    for (int j = 0; j < GN; ++j)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[j][mt][i] = 0.f;
+      for (int i = 0; i < 4; ++i) acc[mt][i] = 0.f;
     for (int r0 = 0; r0 < p.rank; r0 += 16 * AHEAD) {
-      uint2 now[GN][AHEAD][4];
+      uint2 now[AHEAD][4];
 #pragma unroll
-      for (int j = 0; j < GN; ++j)
+      for (int u = 0; u < AHEAD; ++u)
 #pragma unroll
-        for (int u = 0; u < AHEAD; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[j][u][i] = b[j][u][i];
+        for (int i = 0; i < 4; ++i) now[u][i] = b[u][i];
       if (r0 + 16 * AHEAD < p.rank) load_b(r0 + 16 * AHEAD);
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u) {
         const int r = r0 + u * 16;
         if (r >= p.rank) break;
+        const uint32_t m0[4] = {now[u][0].x, now[u][1].x, now[u][0].y, now[u][1].y};
+        const uint32_t m1[4] = {now[u][2].x, now[u][3].x, now[u][2].y, now[u][3].y};
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint2 h = *reinterpret_cast<const uint2*>(planes + (term * 8 + g) * pstride + r + q * 4);
-#pragma unroll
-          for (int j = 0; j < GN; ++j) {
-            const uint32_t m0[4] = {now[j][u][0].x, now[j][u][1].x, now[j][u][0].y, now[j][u][1].y};
-            const uint32_t m1[4] = {now[j][u][2].x, now[j][u][3].x, now[j][u][2].y, now[j][u][3].y};
-            mma16<BF16>(acc[j][0], m0, h.x, h.y);
-            mma16<BF16>(acc[j][1], m1, h.x, h.y);
-          }
+          mma16<BF16>(acc[0], m0, h.x, h.y);
+          mma16<BF16>(acc[1], m1, h.x, h.y);
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < GN; ++j) {
-      const int f = (e + j * step) * 32 + 4 * g;
-      if (e + j * step >= e1) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = q * 2 + i;
-        if (c >= cnt || f >= p.n) continue;
-        const float s = mul[c];
-        float4 v = yv[j][i];
-        v.x = fmaf(acc[j][0][i], s, v.x);
-        v.y = fmaf(acc[j][0][2 + i], s, v.y);
-        v.z = fmaf(acc[j][1][i], s, v.z);
-        v.w = fmaf(acc[j][1][2 + i], s, v.w);
-        float* dst = p.out + tok[c] * p.out_stride + f;
-        if (VEC && f + 4 <= p.n) {
-          *reinterpret_cast<float4*>(dst) = v;
-        } else {
-          dst[0] = v.x;
-          if (f + 1 < p.n) dst[1] = v.y;
-          if (f + 2 < p.n) dst[2] = v.z;
-          if (f + 3 < p.n) dst[3] = v.w;
-        }
+    for (int i = 0; i < 2; ++i) {
+      const int c = q * 2 + i;
+      if (c >= cnt || f >= p.n) continue;
+      const float s = mul[c];
+      float4 v = yv[i];
+      v.x = fmaf(acc[0][i], s, v.x);
+      v.y = fmaf(acc[0][2 + i], s, v.y);
+      v.z = fmaf(acc[1][i], s, v.z);
+      v.w = fmaf(acc[1][2 + i], s, v.w);
+      float* dst = p.out + tok[c] * p.out_stride + f;
+      if (VEC && f + 4 <= p.n) {
+        *reinterpret_cast<float4*>(dst) = v;
+      } else {
+        dst[0] = v.x;
+        if (f + 1 < p.n) dst[1] = v.y;
+        if (f + 2 < p.n) dst[2] = v.z;
+        if (f + 3 < p.n) dst[3] = v.w;
       }
     }
   }

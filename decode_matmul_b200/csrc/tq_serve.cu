@@ -274,7 +274,9 @@ int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t qkv_str
   p.interleaved = interleaved;
   p.status = status_word(workspace_d);
   const int units = (q_heads + 2 * cache->kv_heads) * (cache->head_dim / 16);
-  // many tokens: whole tokens to as many blocks as run at once; few: their heads are spread over blocks
+  // many tokens: whole tokens to as many blocks as run at once; few: their heads are spread over blocks.
+  // Whole against spread (32/8 heads x 128, fp16): 32 tokens 3.6 against 2.7 us, 256 4.4 and 4.5, 518 6.2 and 6.6,
+  // 2000 16.2 against 18.5; e4m3: 32 tokens 5.0 against 3.9, 400 8.2 and 7.6, 700 8.5 against 10.0, 2000 19.5 against 23.3
   const int32_t at_once = sms * tq::append_blocks(cache->dtype);
   const bool many = m >= at_once / 2;
   const int parts = many ? 1 : (units + tq::AP_THREADS - 1) / tq::AP_THREADS;
