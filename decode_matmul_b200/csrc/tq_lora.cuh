@@ -380,7 +380,7 @@ __device__ __forceinline__ void lora_expand8(const LoraParams& p, int32_t ad, in
         const uint32_t m0[4] = {now[u][0].x, now[u][1].x, now[u][0].y, now[u][1].y};
         const uint32_t m1[4] = {now[u][2].x, now[u][3].x, now[u][2].y, now[u][3].y};
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term) {
+        for (int term = TERMS - 1; term >= 0; --term) {  // small terms first
           const uint2 h = *reinterpret_cast<const uint2*>(planes + (term * 8 + g) * pstride + r + q * 4);
           mma16<BF16>(acc[0], m0, h.x, h.y);
           mma16<BF16>(acc[1], m1, h.x, h.y);
@@ -806,15 +806,15 @@ __global__ void __launch_bounds__(LORA_THREADS, PANELS == 1 ? 3 : 2) lora_expand
       if (tid < 4 * kLoraTile && t < t1 && c < cnt && f < p.n)
         asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p.y + sm.yoff[c] + f));
     };
-    auto multiply = [&](int buf) {  // one thread
+    auto multiply = [&](int buf) {  // one thread; small terms first, since each sum loses the bits below its last place
       tc_fence_after();
       const uint32_t d = tmem + (it & 1) * kLoraTile;
-      for (int k = 0; k < steps; ++k) {
-        const uint64_t a = umma_smem_desc(smem_u32(sm.b[buf]) + (k >> 2) * S::PANEL_B + (k & 3) * 32);
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term)
-          umma_f16(d, a, umma_smem_desc(smem_u32(sm.terms[term]) + (k >> 2) * S::PANEL_H + (k & 3) * 32), IDESC, k + term > 0);
-      }
+      for (int term = TERMS - 1; term >= 0; --term)
+        for (int k = 0; k < steps; ++k)
+          umma_f16(d, umma_smem_desc(smem_u32(sm.b[buf]) + (k >> 2) * S::PANEL_B + (k & 3) * 32),
+                   umma_smem_desc(smem_u32(sm.terms[term]) + (k >> 2) * S::PANEL_H + (k & 3) * 32), IDESC,
+                   term < TERMS - 1 || k > 0);
       umma_commit(bar + 8 * (it & 1));
     };
     // the operand terms of the tokens (zeros for those that are not there), 8 ranks at a time
