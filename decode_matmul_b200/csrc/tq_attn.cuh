@@ -18,8 +18,8 @@
 // so that the 8-wide side of the MMA is the heads and none of the 16-wide
 // side is padding; P^T's operand layout is the transpose of S^T's result
 // layout (movmatrix).  Warp MMAs suffice: at the cache's bandwidth they need
-// about a tenth of their rate, and the one-row-per-key layout they take needs
-// no tensor map, so any page size and strides work.
+// a fifth (bf16) to a quarter (e4m3) of their rate, and the one-row-per-key
+// layout they take needs no tensor map, so any page size and strides work.
 // Items (row, key head, head group) that a warp holds whole are written by
 // it.  The others leave partial (O, M, L), joined first inside the block, then
 // over the blocks by the last to arrive, in a fixed order (the same bits on
@@ -28,7 +28,8 @@
 // the first tile 1.5 us (4 us from HBM), the joins 2 to 5 us; between them the
 // warps stream at 7 TB/s.  Measured, three caches in turn: 64 rows of 3 to 8192
 // keys, 8 heads x 128 bf16: 72 us, 5.2 TB/s; 16 rows of 20000 to 65536 e4m3
-// keys: 248 us, 5.5 TB/s; one row of 777 keys: 10 us.
+// keys: 262 us, 5.2 TB/s (0.44 instructions per scheduler and cycle from two
+// warps: their own latencies bound it); one row of 777 keys: 10 us.
 #pragma once
 
 #include "tq_kv.cuh"

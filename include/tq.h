@@ -451,7 +451,9 @@ TQ_API int tq_kv_append(const tq_kv_cache_t* cache, const float* qkv_d, int64_t 
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) V_j
  * q_d: [m][q_heads][head_dim], bf16 for a bf16 cache, else fp16.  out_d: the
  *   same layout, out_dtype TQ_BF16 (phase 1's input) or TQ_F16.  Scores,
- *   maxima, sums and outputs are fp32 until the last rounding.
+ *   maxima, sums and outputs are fp32 until the last rounding; softmax weights
+ *   keep 22 bits (fp16 and e4m3 caches, in steps of 2^-39 of the largest) or
+ *   24 (bf16).
  * A row that sees no key (pos_d[t] < 0: a padded row) gives zeros.  Cache
  *   bytes of positions that no row sees are not used, whatever they hold.
  *   An infinite value that is seen gives its infinity, unless its weight
