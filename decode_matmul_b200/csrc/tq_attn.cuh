@@ -69,7 +69,6 @@ struct AttnCfg {
   static constexpr int KT = TK / 16;
   static constexpr int STAGE = 2 * TK * RB;  // the keys, then the values
   static constexpr int COLS = 8 * NT;        // head columns
-  static constexpr int TERMS = T == KV_BF16 ? 3 : 2;  // of a weight (AttnWeights)
   static constexpr int PART = D * COLS + 2 * COLS;  // floats of a partial: O [D][COLS], M, L
   static constexpr int SLOT = PART * 4;
   static constexpr int CTL = 2048;
@@ -141,12 +140,13 @@ __device__ __forceinline__ void mma16(float c[4], const uint32_t a[4], uint32_t 
 }
 
 // The weights of the second product as MMA operands.  They are at most 2^UP and
-// the sum of two keys' terms (a pair in each word) is the binary32 weight:
-// three bf16 terms (24 bits), or two fp16 terms (22 bits).  UP = 15 for fp16:
-// its smallest step, 2^-24, then is 2^-39 of the largest weight; with weights of
-// at most 1 a key of less than 2^-25 would add nothing to O while the sum of the
-// weights still counted it (16384 keys 18 below one key in e^s: all of their
-// part of the output lost).  O and the sum carry the same 2^UP, which cancels.
+// the sum of a weight's terms (each word has those of two weights) keeps
+// binary32 accuracy: three bf16 terms (24 bits) or two fp16 terms (22 bits).
+// UP = 15 for fp16: its smallest step, 2^-24, then is 2^-39 of the largest
+// weight; with weights of at most 1 a key of less than 2^-25 would add nothing
+// to O while the sum of the weights still counted it (16384 keys 18 below one
+// key in e^s: all of their part of the output lost).  O and the sum carry the
+// same 2^UP, which cancels.
 // With one fp16 term (2^-12) or two of bf16 (2^-17) 6 to 10%, or 0.2%, of the bf16
 // outputs were rounded to the other neighbour.
 // For 16-bit caches every term of a weight is positive: an infinite value then
@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
   constexpr bool BF = T == KV_BF16;
   constexpr bool F8 = T == KV_E4M3;
   constexpr int W = C::WARPS, S = C::STAGES, COLS = C::COLS, MT = D / 16, TK = C::TK, KT = C::KT;
+  constexpr int TERMS = AttnWeights<T>::TERMS;
   extern __shared__ __align__(16) uint8_t smem[];
   struct Part {  // what a warp left in a slot
     int32_t first, n, row, item;  // unit of the item's first tile, its tiles (0: nothing)
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
             }
         }
         // P^T as the B operand, in terms that keep binary32 accuracy (AttnWeights)
-        uint32_t pt[C::TERMS][KT][NT][2];
+        uint32_t pt[TERMS][KT][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float m0[2];
@@ -790,10 +791,10 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
                 e[i] = vm == FULL_MASK || x != -INFINITY ? ex2(fmaf(x, sc, m0[i])) : 0.f;
                 sum[nt][i] += e[i];
               }
-              uint32_t t[C::TERMS];
+              uint32_t t[TERMS];
               AttnWeights<T>::split(e[0], e[1], t);
 #pragma unroll
-              for (int k = 0; k < C::TERMS; ++k) pt[k][kt][nt][r] = transpose8(t[k]);
+              for (int k = 0; k < TERMS; ++k) pt[k][kt][nt][r] = transpose8(t[k]);
             }
         }
         // O^T: the tile's share, two row tiles at a time, is added to O by the
@@ -830,7 +831,7 @@ __global__ void __launch_bounds__(AttnCfg<T, D, NT>::THREADS, 1) attn_kernel(con
               }
             }
 #pragma unroll
-            for (int k = C::TERMS - 1; k >= 0; --k)
+            for (int k = TERMS - 1; k >= 0; --k)
 #pragma unroll
               for (int u = 0; u < 2; ++u)
 #pragma unroll
